@@ -417,3 +417,10 @@ def puro_fp8_cast_e4m3(v, q=None, stream=None):
     _need(q, "q", torch.uint8, tuple(v.shape), whole=True)
     _check(lib.puro_fp8_cast_e4m3(_ptr(v), v.numel(), _ptr(q), _stream(stream)), "puro_fp8_cast_e4m3")
     return q
+
+
+# the operators around the linear layer (puro_ops.h)
+from .ops import *  # noqa: E402,F401,F403
+from .ops import __all__ as _ops_all  # noqa: E402
+
+__all__ += _ops_all

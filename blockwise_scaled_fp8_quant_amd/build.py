@@ -22,7 +22,8 @@ OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpuro_fp8.so")
 ARCH = "gfx950"
 
-SOURCES = ["quant.hip", "gemm.hip", "gemm_w4.hip", "abi.cpp"]
+SOURCES = ["quant.hip", "gemm.hip", "gemm_w4.hip", "abi.cpp",
+           "norm.hip", "clip.hip", "gemm_rows.hip", "abi_ops.cpp"]
 
 
 def _hipcc() -> str:

@@ -1,0 +1,605 @@
+// gfx950 layer / RMS norm: forward (as a tensor, as 1x128 FP8 codes, as 1x128 and transposed 128x1
+// codes) and backward with the reduction of the weight's and bias's gradient.
+//
+// Mathematics, for a row x of C columns:
+//   mu = mean(x) (RMS: 0),  r = 1 / sqrt(mean((x - mu)^2) + eps),  xh = (x - mu) r,  y = xh g + b
+//   u = dy g:  dx = r (u - mean(u) - xh mean(u xh)) (RMS: without mean(u));  dg = sum_t dy xh;  db = sum_t dy
+// All of it is bound by HBM: one read of x (and dy) and one write.  A row is therefore held in
+// registers between its statistics and its use, and a thread keeps the same columns for every row it
+// takes, so the weight, the bias and the weight gradient's sums stay in registers too.
+//
+// Statistics are fp32: a thread adds its at most 32 values of the row in order, then the lanes and waves are joined
+// in a tree; the variance is the mean square of the differences from the mean.  y, dx are rounded
+// once.  dg and db are summed in fp32: at most a few tens of rows in order per thread, then waves and
+// workgroups in a fixed order.
+#include "codec.hpp"
+#include "gemm_args.hpp"
+#include "ops_internal.hpp"
+
+#include <algorithm>
+
+namespace puro {
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// ---- eight consecutive columns of a row -------------------------------------------------------------
+// VEC: 16-byte aligned, either all eight exist or none.  Otherwise element by element, nv of them.
+template <bool BF16>
+struct Raw8;
+template <>
+struct Raw8<true> {
+  u32x4 w;
+};
+template <>
+struct Raw8<false> {
+  u32x4 w[2];
+};
+
+template <bool BF16, bool VEC>
+__device__ __forceinline__ Raw8<BF16> load8(const void* base, int64_t at, int nv) {
+  Raw8<BF16> r;
+  if constexpr (BF16) {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+    r.w = u32x4{0u, 0u, 0u, 0u};
+    if constexpr (VEC) {
+      if (nv > 0) r.w = *reinterpret_cast<const u32x4*>(p);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < nv) r.w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+    }
+  } else {
+    const uint32_t* p = static_cast<const uint32_t*>(base) + at;
+    r.w[0] = r.w[1] = u32x4{0u, 0u, 0u, 0u};
+    if constexpr (VEC) {
+      if (nv > 0) {
+        r.w[0] = *reinterpret_cast<const u32x4*>(p);
+        r.w[1] = *reinterpret_cast<const u32x4*>(p + 4);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < nv) r.w[j >> 2][j & 3] = p[j];
+    }
+  }
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const Raw8<BF16>& r, float v[8]) {
+  if constexpr (BF16) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (j & 1) ? bf16_hi(r.w[j >> 1]) : bf16_lo(r.w[j >> 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r.w[j >> 2][j & 3]);
+  }
+}
+
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void store8(void* base, int64_t at, int nv, const float v[8]) {
+  if constexpr (BF16) {
+    const u32x4 o = {bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
+    uint16_t* p = static_cast<uint16_t*>(base) + at;
+    if constexpr (VEC) {
+      if (nv > 0) __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(p));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < nv) p[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+    }
+  } else {
+    float* p = static_cast<float*>(base) + at;
+    if constexpr (VEC) {
+      if (nv > 0) {
+        __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
+        __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(p + 4));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < nv) p[j] = v[j];
+    }
+  }
+}
+
+// Eight values of a weight or bias vector (read once per thread and launch; any alignment).
+__device__ __forceinline__ void load_vec8(const void* base, bool bf16, int col, int nv, float v[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = 0.f;
+    if (j < nv)
+      v[j] = bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t*>(base)[col + j] << 16)
+                  : static_cast<const float*>(base)[col + j];
+  }
+}
+
+// ---- sums over the lanes of a wave and the waves of a team -------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<kDppQuadXor1>(v);
+  v = dpp_add<kDppQuadXor2>(v);
+  v = dpp_add<kDppRowHalfMirror>(v);
+  v = dpp_add<kDppRowMirror>(v);
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  return v;
+}
+
+// Sum over a team of WPR waves; every lane gets it.  `slot` is one of two LDS rows used in turn, so a
+// wave that runs ahead into the next sum does not overwrite what a slower one still reads (the
+// barrier of the next sum is between them).
+template <int WPR, int WAVES>
+__device__ __forceinline__ float team_sum(float v, float (*red)[WAVES], int slot, int wave) {
+  v = wave_sum(v);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 63) == 0) red[slot][wave] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) v += red[slot][(wave / WPR) * WPR + w];
+  }
+  return v;
+}
+
+// scale and multiplier of a group from the bits of its fp32 maximum (sign cleared), as tile_scale
+__device__ __forceinline__ void tile_scale32(uint32_t amax_bits, float& s, float& r) {
+  const float a = __uint_as_float(umax(amax_bits, kAmaxFloorBf16 << 16));
+  s = a / kE4M3Max;
+  r = kE4M3Max / a;
+}
+
+// ---------------------------------------------------------------------------------------------------
+// Forward.  A team of WPR waves takes a row, each thread ITER chunks of eight columns, chunk i of team
+// thread t at column 8 (64 WPR i + t): 16-byte loads that are contiguous over a wave, and 16 lanes
+// hold one 128-column group.  A team takes rows_per_team consecutive rows (the 32-row run of a
+// workgroup then fills whole lines of the row-wise scale and statistics arrays) and loads the next
+// row before it works on the present one.
+// WHAT: 0 y, 1 codes and scales, 2 the statistics alone (first launch of the dual form).
+// ---------------------------------------------------------------------------------------------------
+template <bool BF16, bool VEC, int WPR, int ITER, int WHAT>
+__global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs a) {
+  constexpr int kWaves = WPR > 4 ? WPR : 4;
+  constexpr int kTeams = kWaves / WPR;
+  constexpr int kTeamThreads = 64 * WPR;
+  __shared__ float red[2][kWaves];
+  const int wave = threadIdx.x >> 6;
+  const int team = wave / WPR;
+  const int tt = threadIdx.x - team * kTeamThreads;
+  const int64_t row0 = ((int64_t)blockIdx.x * kTeams + team) * a.rows_per_team;
+
+  int col[ITER], nv[ITER];
+  float g[ITER][8], b[ITER][8];
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    col[i] = 8 * (kTeamThreads * i + tt);
+    nv[i] = a.C - col[i] < 0 ? 0 : (a.C - col[i] > 8 ? 8 : a.C - col[i]);
+    if constexpr (WHAT != 2) {
+      load_vec8(a.gamma, a.w_bf16, col[i], nv[i], g[i]);
+      load_vec8(a.beta, a.w_bf16, col[i], a.beta ? nv[i] : 0, b[i]);
+    }
+  }
+  const float inv_c = 1.0f / (float)a.C;
+  Raw8<BF16> next[ITER];
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) next[i] = load8<BF16, VEC>(a.x, row0 * a.ldx + col[i], row0 < a.T ? nv[i] : 0);
+
+  for (int k = 0; k < a.rows_per_team; ++k) {
+    const int64_t row = row0 + k;
+    const bool ok = row < a.T;
+    float v[ITER][8];
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) unpack8<BF16>(next[i], v[i]);
+    if (k + 1 < a.rows_per_team) {
+#pragma unroll
+      for (int i = 0; i < ITER; ++i)
+        next[i] = load8<BF16, VEC>(a.x, (row + 1) * a.ldx + col[i], row + 1 < a.T ? nv[i] : 0);
+    }
+    float mean = 0.f;
+    if (a.layer) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < ITER; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += v[i][j];   // missing columns were loaded as zero
+      mean = team_sum<WPR, kWaves>(sum, red, 0, wave) * inv_c;
+    }
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      float part = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] -= mean;
+        if constexpr (VEC)
+          part = __builtin_fmaf(v[i][j], v[i][j], part);
+        else
+          part = j < nv[i] ? __builtin_fmaf(v[i][j], v[i][j], part) : part;
+      }
+      sq += nv[i] > 0 ? part : 0.f;
+    }
+    const float rstd = 1.0f / __builtin_sqrtf(team_sum<WPR, kWaves>(sq, red, 1, wave) * inv_c + a.eps);
+    if (ok && tt == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    if constexpr (WHAT != 2) {
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(v[i][j] * rstd, g[i][j], b[i][j]);
+        if constexpr (WHAT == 0) {
+          store8<BF16, VEC>(a.y, row * a.ldy + col[i], ok ? nv[i] : 0, y);
+        } else {
+          uint32_t m = 0u;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = umax(m, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+          float sc, r;
+          tile_scale32(row16_max(m), sc, r);
+          if (ok && nv[i] > 0) {
+            const u32x2 o = {cvt4(y[0] * r, y[1] * r, y[2] * r, y[3] * r), cvt4(y[4] * r, y[5] * r, y[6] * r, y[7] * r)};
+            __builtin_nontemporal_store(o, reinterpret_cast<u32x2*>(a.q + row * a.ldq + col[i]));
+            if ((tt & 15) == 0) a.s[(int64_t)(col[i] >> 7) * a.T + row] = sc;
+          }
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------------
+// Second launch of the dual form: a 128-row x 128-column tile per workgroup, as quant_dual_kernel
+// (quant.hip) on the norm formed in registers from x and the statistics of the first launch.  x is
+// read twice (once per launch); keeping 128 whole rows on one CU for a single read does not fit
+// beyond a few hundred columns.
+// ---------------------------------------------------------------------------------------------------
+template <bool BF16>
+__global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a, int bt) {
+  __shared__ uint32_t rowmax[128];
+  __shared__ uint32_t colred[4][128];
+  __shared__ float rrow[128], rcol[128];
+  __shared__ uint32_t stage[128 * 33];
+
+  const int t = threadIdx.x;
+  const int lane = t & 63, wave = t >> 6;
+  const int tc = t & 15, tr = t >> 4;
+  const int64_t b = blockIdx.x;
+  const int64_t run = b / bt, ncb = a.C / 128;
+  const int64_t tb = (run / ncb) * bt + (b - run * bt);
+  const int64_t gcol = run % ncb;
+  const int64_t tok0 = tb * 128 + tr * 8;
+  const int col0 = (int)gcol * 128 + tc * 8;
+
+  Raw8<BF16> raw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) raw[i] = load8<BF16, true>(a.x, (tok0 + i) * a.ldx + col0, 8);
+  float g[8], be[8];
+  load_vec8(a.gamma, a.w_bf16, col0, 8, g);
+  load_vec8(a.beta, a.w_bf16, col0, a.beta ? 8 : 0, be);
+
+  float y[8][8];
+  uint32_t cm[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float mean = a.layer ? a.mean[tok0 + i] : 0.f, rstd = a.rstd[tok0 + i];
+    unpack8<BF16>(raw[i], y[i]);
+    uint32_t m = 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      y[i][j] = __builtin_fmaf((y[i][j] - mean) * rstd, g[j], be[j]);
+      const uint32_t bits = __float_as_uint(y[i][j]) & 0x7FFFFFFFu;
+      m = umax(m, bits);
+      cm[j] = umax(cm[j], bits);
+    }
+    m = row16_max(m);
+    if (tc == 0) rowmax[tr * 8 + i] = m;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    cm[j] = umax(cm[j], (uint32_t)__shfl_xor((int)cm[j], 16));
+    cm[j] = umax(cm[j], (uint32_t)__shfl_xor((int)cm[j], 32));
+  }
+  if (lane < 16) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) colred[wave][tc * 8 + j] = cm[j];
+  }
+  __syncthreads();
+  if (t < 128) {
+    float sc, r;
+    tile_scale32(rowmax[t], sc, r);
+    rrow[t] = r;
+    a.s[gcol * a.T + tb * 128 + t] = sc;
+  } else {
+    const int c = t - 128;
+    float sc, r;
+    tile_scale32(umax(umax(colred[0][c], colred[1][c]), umax(colred[2][c], colred[3][c])), sc, r);
+    rcol[c] = r;
+    a.sT[tb * a.C + gcol * 128 + c] = sc;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float r = rrow[tr * 8 + i];
+    const u32x2 o = {cvt4(y[i][0] * r, y[i][1] * r, y[i][2] * r, y[i][3] * r),
+                     cvt4(y[i][4] * r, y[i][5] * r, y[i][6] * r, y[i][7] * r)};
+    __builtin_nontemporal_store(o, reinterpret_cast<u32x2*>(a.q + (tok0 + i) * a.ldq + col0));
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float r = rcol[tc * 8 + j];
+    stage[(tc * 8 + j) * 33 + 2 * tr] = cvt4(y[0][j] * r, y[1][j] * r, y[2][j] * r, y[3][j] * r);
+    stage[(tc * 8 + j) * 33 + 2 * tr + 1] = cvt4(y[4][j] * r, y[5][j] * r, y[6][j] * r, y[7][j] * r);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int cl = (t >> 3) + 32 * it;
+    const int part = t & 7;
+    const uint32_t* sp = stage + cl * 33 + part * 4;
+    const u32x4 o = {sp[0], sp[1], sp[2], sp[3]};
+    __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(a.qT + (gcol * 128 + cl) * a.ldqT + tb * 128 + part * 16));
+  }
+}
+
+// ---------------------------------------------------------------------------------------------------
+// Backward.  Eight waves per workgroup, teams of WPR waves with a row each; thread columns as in the
+// forward kernel.  The weight's and bias's gradient of a thread's columns are summed in registers
+// over the team's rows, then over the workgroup's teams through LDS, and written as the workgroup's
+// partial sums; norm_bwd_reduce_kernel adds those in order.
+// ---------------------------------------------------------------------------------------------------
+constexpr int kBwdThreads = 512;
+constexpr int kBwdWaves = kBwdThreads / 64;
+
+template <bool BF16, bool VEC, int WPR, int ITER>
+__global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, int rows_per_team, bool direct) {
+  constexpr int kTeams = kBwdWaves / WPR;
+  constexpr int kTeamThreads = 64 * WPR;
+  constexpr int kWidth = 8 * kTeamThreads * ITER;
+  __shared__ float red[2][2][kBwdWaves];
+  __shared__ float join[kTeams > 1 ? kTeams * kWidth : 4];
+  const int wave = threadIdx.x >> 6;
+  const int team = wave / WPR;
+  const int tt = threadIdx.x - team * kTeamThreads;
+  const int64_t stride = (int64_t)gridDim.x * kTeams;
+
+  int col[ITER], nv[ITER];
+  float g[ITER][8], dg[ITER][8], db[ITER][8];
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    col[i] = 8 * (kTeamThreads * i + tt);
+    nv[i] = a.C - col[i] < 0 ? 0 : (a.C - col[i] > 8 ? 8 : a.C - col[i]);
+    load_vec8(a.gamma, a.w_bf16, col[i], nv[i], g[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.f;
+  }
+  const float inv_c = 1.0f / (float)a.C;
+  int64_t row = (int64_t)blockIdx.x * kTeams + team;
+  Raw8<BF16> nx[ITER], ny[ITER];
+  float nmean = 0.f, nrstd = 0.f;
+  auto fetch = [&](int64_t r) {
+    const bool ok = r < a.T;
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      nx[i] = load8<BF16, VEC>(a.x, r * a.ldx + col[i], ok ? nv[i] : 0);
+      ny[i] = load8<BF16, VEC>(a.dy, r * a.lddy + col[i], ok ? nv[i] : 0);
+    }
+    nmean = ok && a.layer ? a.mean[r] : 0.f;
+    nrstd = ok ? a.rstd[r] : 0.f;
+  };
+  fetch(row);
+  for (int k = 0; k < rows_per_team; ++k, row += stride) {
+    const bool ok = row < a.T;
+    const float mean = nmean, rstd = nrstd;
+    float xh[ITER][8], d[ITER][8];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      unpack8<BF16>(nx[i], xh[i]);
+      unpack8<BF16>(ny[i], d[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // a column that does not exist has dy = 0 and weight 0: it adds nothing to any sum
+        xh[i][j] = (xh[i][j] - mean) * rstd;
+        dg[i][j] = __builtin_fmaf(d[i][j], xh[i][j], dg[i][j]);
+        db[i][j] += d[i][j];
+        d[i][j] *= g[i][j];
+        s1 += d[i][j];
+        s2 = __builtin_fmaf(d[i][j], xh[i][j], s2);
+      }
+    }
+    if (k + 1 < rows_per_team) fetch(row + stride);
+    s1 = wave_sum(s1);
+    s2 = wave_sum(s2);
+    if constexpr (WPR > 1) {
+      const int slot = k & 1;
+      if ((threadIdx.x & 63) == 0) {
+        red[slot][0][wave] = s1;
+        red[slot][1][wave] = s2;
+      }
+      __syncthreads();
+      s1 = s2 = 0.f;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) {
+        s1 += red[slot][0][team * WPR + w];
+        s2 += red[slot][1][team * WPR + w];
+      }
+    }
+    s1 = a.layer ? s1 * inv_c : 0.f;
+    s2 *= inv_c;
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = (__builtin_fmaf(-xh[i][j], s2, d[i][j]) - s1) * rstd;
+      store8<BF16, VEC>(a.dx, row * a.lddx + col[i], ok ? nv[i] : 0, o);
+    }
+  }
+
+  // the workgroup's sums: first the weight's gradient, then the bias's, through one LDS array
+  float* out_g = direct ? a.dgamma : a.partial + (int64_t)blockIdx.x * 2 * a.C;
+  float* out_b = direct ? a.dbeta : a.partial + ((int64_t)blockIdx.x * 2 + 1) * a.C;
+  const bool add = direct && a.accumulate;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float* out = which == 0 ? out_g : out_b;
+    if (which == 1 && a.dbeta == nullptr) break;
+    if constexpr (kTeams > 1) {
+      if (which == 1) __syncthreads();
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) {
+        f32x4* p = reinterpret_cast<f32x4*>(join + team * kWidth + col[i]);
+        const float* v = which == 0 ? dg[i] : db[i];
+        p[0] = f32x4{v[0], v[1], v[2], v[3]};
+        p[1] = f32x4{v[4], v[5], v[6], v[7]};
+      }
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.C; c += kBwdThreads) {
+        float s = join[c];
+#pragma unroll
+        for (int w = 1; w < kTeams; ++w) s += join[w * kWidth + c];
+        out[c] = add ? out[c] + s : s;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < ITER; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float s = which == 0 ? dg[i][j] : db[i][j];
+          if (j < nv[i]) out[col[i] + j] = add ? out[col[i] + j] + s : s;
+        }
+    }
+  }
+}
+
+// dgamma[c], dbeta[c] = sum over workgroups of their partials: 16 columns x 16 runs of workgroups per
+// workgroup, the runs joined in order.
+__global__ __launch_bounds__(256) void norm_bwd_reduce_kernel(const float* __restrict__ partial, int blocks, int C,
+                                                              float* dgamma, float* dbeta, int accumulate) {
+  __shared__ float part[16][17];
+  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + cx;
+  const int which = blockIdx.y;
+  float s = 0.f;
+  if (c < C)
+    for (int b = ry; b < blocks; b += 16) s += partial[((int64_t)b * 2 + which) * C + c];
+  part[ry][cx] = s;
+  __syncthreads();
+  if (ry == 0 && c < C) {
+#pragma unroll
+    for (int r = 1; r < 16; ++r) s += part[r][cx];
+    float* out = which == 0 ? dgamma : dbeta;
+    out[c] = accumulate ? out[c] + s : s;
+  }
+}
+
+__global__ __launch_bounds__(256) void norm_zero_kernel(float* dgamma, float* dbeta, int C) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= C) return;
+  dgamma[c] = 0.f;
+  if (dbeta) dbeta[c] = 0.f;
+}
+
+inline bool vec_row(const void* p, int64_t ld, int64_t es) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * es) % 16 == 0;
+}
+
+template <bool BF16, bool VEC, int WHAT>
+hipError_t launch_fwd(NormArgs a, hipStream_t st) {
+  // The layout over threads goes by C alone, so every form sums a row in the same order.
+  auto go = [&](auto kernel, int wpr) {
+    const int waves = wpr > 4 ? wpr : 4, teams = waves / wpr;
+    // rows per team: 8 for long inputs, so that a workgroup's 32 rows fill whole lines of the row-wise
+    // arrays; one row where the input would not fill the card otherwise
+    int64_t r = std::max<int64_t>(1, std::min<int64_t>(8, a.T / (2048 / wpr)));
+    a.rows_per_team = (int)r;
+    const int64_t blocks = (a.T + teams * r - 1) / (teams * r);
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(64 * waves), 0, st, a);
+    return hipGetLastError();
+  };
+  if (a.C <= 512) return go(norm_kernel<BF16, VEC, 1, 1, WHAT>, 1);
+  if (a.C <= 1024) return go(norm_kernel<BF16, VEC, 1, 2, WHAT>, 1);
+  if (a.C <= 2048) return go(norm_kernel<BF16, VEC, 1, 4, WHAT>, 1);
+  if (a.C <= 4096) return go(norm_kernel<BF16, VEC, 2, 4, WHAT>, 2);
+  if (a.C <= 8192) return go(norm_kernel<BF16, VEC, 4, 4, WHAT>, 4);
+  return go(norm_kernel<BF16, VEC, 8, 4, WHAT>, 8);
+}
+
+// waves per row of the backward kernel; its rows per workgroup and step are kBwdWaves / this
+int bwd_wpr(int64_t C) { return C <= 2048 ? 1 : C <= 4096 ? 2 : C <= 8192 ? 4 : 8; }
+
+template <bool BF16, bool VEC>
+hipError_t launch_bwd(const NormBwdArgs& a, hipStream_t st) {
+  const int blocks = norm_bwd_blocks(a.T, a.C);
+  const int teams = kBwdWaves / bwd_wpr(a.C);
+  const int rows = (int)((a.T + (int64_t)blocks * teams - 1) / ((int64_t)blocks * teams));
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kBwdThreads), 0, st, a, rows, blocks == 1);
+    return hipGetLastError();
+  };
+  hipError_t e;
+  if (a.C <= 512) e = go(norm_bwd_kernel<BF16, VEC, 1, 1>);
+  else if (a.C <= 1024) e = go(norm_bwd_kernel<BF16, VEC, 1, 2>);
+  else if (a.C <= 2048) e = go(norm_bwd_kernel<BF16, VEC, 1, 4>);
+  else if (a.C <= 4096) e = go(norm_bwd_kernel<BF16, VEC, 2, 4>);
+  else if (a.C <= 8192) e = go(norm_bwd_kernel<BF16, VEC, 4, 4>);
+  else e = go(norm_bwd_kernel<BF16, VEC, 8, 4>);
+  if (e != hipSuccess || blocks == 1) return e;
+  hipLaunchKernelGGL(norm_bwd_reduce_kernel, dim3((unsigned)((a.C + 15) / 16), a.dbeta ? 2 : 1), dim3(256), 0, st,
+                     a.partial, blocks, a.C, a.dgamma, a.dbeta, a.accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm(NormArgs a, hipStream_t st) {
+  const int64_t es = a.x_bf16 ? 2 : 4;
+  const bool vec = a.C % 8 == 0 && vec_row(a.x, a.ldx, es) && vec_row(a.y, a.ldy, es);
+  if (a.x_bf16) return vec ? launch_fwd<true, true, 0>(a, st) : launch_fwd<true, false, 0>(a, st);
+  return vec ? launch_fwd<false, true, 0>(a, st) : launch_fwd<false, false, 0>(a, st);
+}
+
+hipError_t launch_norm_quant(NormArgs a, hipStream_t st) {
+  return a.x_bf16 ? launch_fwd<true, true, 1>(a, st) : launch_fwd<false, true, 1>(a, st);
+}
+
+hipError_t launch_norm_quant_dual(NormArgs a, hipStream_t st) {
+  const hipError_t e = a.x_bf16 ? launch_fwd<true, true, 2>(a, st) : launch_fwd<false, true, 2>(a, st);
+  if (e != hipSuccess) return e;
+  const int64_t nb = a.T / 128;
+  int bt = 32;   // token blocks per run of workgroups: transposed rows are written in runs (quant.hip, tile_order)
+  while (nb % bt) bt >>= 1;
+  const dim3 grid((unsigned)(nb * (a.C / 128)));
+  if (a.x_bf16)
+    hipLaunchKernelGGL(norm_dual_kernel<true>, grid, dim3(256), 0, st, a, bt);
+  else
+    hipLaunchKernelGGL(norm_dual_kernel<false>, grid, dim3(256), 0, st, a, bt);
+  return hipGetLastError();
+}
+
+int norm_bwd_blocks(int64_t T, int64_t C) {
+  if (T <= 0 || C <= 0) return 0;
+  const int teams = kBwdWaves / bwd_wpr(C);
+  return (int)std::min<int64_t>(256, (T + 2 * teams - 1) / (2 * teams));
+}
+
+hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t st) {
+  if (a.T == 0 || a.C == 0) {
+    if (a.accumulate || a.C == 0) return hipSuccess;
+    hipLaunchKernelGGL(norm_zero_kernel, dim3((unsigned)((a.C + 255) / 256)), dim3(256), 0, st, a.dgamma, a.dbeta, a.C);
+    return hipGetLastError();
+  }
+  const int64_t es = a.x_bf16 ? 2 : 4;
+  const bool vec = a.C % 8 == 0 && vec_row(a.x, a.ldx, es) && vec_row(a.dy, a.lddy, es) && vec_row(a.dx, a.lddx, es);
+  if (a.x_bf16) return vec ? launch_bwd<true, true>(a, st) : launch_bwd<true, false>(a, st);
+  return vec ? launch_bwd<false, true>(a, st) : launch_bwd<false, false>(a, st);
+}
+
+}  // namespace puro

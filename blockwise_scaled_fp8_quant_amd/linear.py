@@ -22,7 +22,9 @@ puro_fp8_gemm_accumulate and no .grad is produced; otherwise the fp32 dW is retu
 autograd stores it in the weight's dtype.
 
 Shapes follow the kernels: Din, Dout and the number of tokens (product of X's leading
-dimensions) must be multiples of 128; anything else raises PuroError (PURO_ERR_SHAPE).
+dimensions) must be multiples of 128; anything else raises PuroError (PURO_ERR_SHAPE).  Without
+gradients (torch.no_grad) the number of tokens is free: a ragged one runs puro_gemm_rows, and so
+does a caller that keeps the weight's codes over many calls (Fp8Linear.quantize_weight).
 """
 from __future__ import annotations
 
@@ -31,7 +33,7 @@ import math
 import torch
 
 from . import (DGRAD, FWD, OUT_BF16, OUT_FP32, WGRAD, puro_fp8_gemm, puro_fp8_gemm_accumulate,
-               puro_fp8_quant_act_dual, puro_fp8_quant_w_128x128)
+               puro_fp8_quant_act_1x128, puro_fp8_quant_act_dual, puro_fp8_quant_w_128x128, puro_gemm_rows)
 
 __all__ = ["Fp8LinearFunction", "Fp8Linear", "fp8_linear"]
 
@@ -101,8 +103,23 @@ class Fp8Linear(torch.nn.Module):
         self.weight.main_grad = torch.zeros(self.weight.shape, dtype=torch.float32, device=self.weight.device)
         return self.weight.main_grad
 
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
-        return Fp8LinearFunction.apply(x, self.weight)
+    def quantize_weight(self):
+        """(codes, scales) of the weight, for `codes` of forward: kept by a caller that runs many steps on
+        one weight, and made anew when the weight changes."""
+        return puro_fp8_quant_w_128x128(_rows(self.weight.detach(), self.in_features), transposed=False)[:2]
+
+    def forward(self, x: torch.Tensor, codes=None) -> torch.Tensor:
+        if codes is None and (torch.is_grad_enabled() or (x.numel() // max(self.in_features, 1)) % 128 == 0):
+            return Fp8LinearFunction.apply(x, self.weight)
+        if torch.is_grad_enabled():
+            raise ValueError("codes: a weight quantized beforehand is for use without gradients (torch.no_grad)")
+        if x.dtype != torch.bfloat16:
+            raise TypeError("Fp8Linear takes bf16 activations and bf16 weights")
+        if x.shape[-1] != self.in_features:
+            raise ValueError(f"x has {x.shape[-1]} features, weight expects {self.in_features}")
+        wq, ws = self.quantize_weight() if codes is None else codes
+        xq, xs = puro_fp8_quant_act_1x128(_rows(x, self.in_features))
+        return puro_gemm_rows(xq, xs, wq, ws).view(*x.shape[:-1], self.out_features)
 
     def extra_repr(self) -> str:
         return f"in_features={self.in_features}, out_features={self.out_features}, fp8=blockwise"

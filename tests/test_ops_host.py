@@ -1,0 +1,201 @@
+"""Host-side checks of include/puro_ops.h (no GPU, no kernel launched): the header, the binding and the library
+name the same entry points; every call below has an invalid argument or an empty shape, so the library returns
+before any HIP call."""
+import ctypes
+import math
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+import blockwise_scaled_fp8_quant_amd as P
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "puro_ops.h")
+OK, NULLPTR, SHAPE, ALIGN, LD, MODE, DTYPE, WORKSPACE, UNSUP, ARG = 0, -1, -2, -3, -4, -5, -6, -7, -9, -10
+A16, MIS = 0x10000, 0x10008       # never dereferenced: validation fails first
+BF16, FP32 = 0, 1
+
+
+def declared():
+    src = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    return sorted(set(re.findall(r"\b(puro_\w+)\s*\(", src)))
+
+
+def test_header_binding_and_library_agree():
+    assert sorted(P.EXPORTED_OPS) == declared()
+    out = subprocess.run(["nm", "-D", "--defined-only", P.LIB_PATH], capture_output=True, text=True).stdout
+    for name in declared():
+        assert re.search(rf"\bT {name}\b", out), name
+        assert hasattr(P, name) or name == "puro_grad_norm_workspace_size"
+    assert P.puro_fp8_strerror(ARG) != "unknown status"
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="no C compiler")
+def test_header_is_strict_c11(tmp_path):
+    src = tmp_path / "p.c"
+    src.write_text('#include "puro_ops.h"\nint main(void) { puro_grad_job j = {0}; return j.n != 0; }\n')
+    r = subprocess.run(["gcc", "-std=c11", "-Wall", "-Wextra", "-Werror", "-pedantic", "-I",
+                        os.path.join(ROOT, "include"), "-c", str(src), "-o", str(tmp_path / "p.o")],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def norm(kind=0, xd=BF16, x=A16, T=4, C=256, ldx=256, wd=BF16, w=A16, b=A16, eps=1e-5, y=A16, ldy=256, mean=A16,
+         rstd=A16):
+    return P.lib.puro_layer_norm(kind, xd, x, T, C, ldx, wd, w, b, eps, y, ldy, mean, rstd, None)
+
+
+def test_norm_refusals():
+    assert norm(T=0) == OK and norm(C=0) == OK and norm(T=0, x=None, y=None) == OK
+    assert norm(kind=2) == MODE and norm(xd=2) == DTYPE and norm(wd=-1) == DTYPE
+    assert norm(T=-1) == SHAPE and norm(C=-1) == SHAPE
+    for eps in (-1e-5, math.nan, math.inf):
+        assert norm(eps=eps) == ARG
+    assert norm(kind=1) == ARG                                   # an RMS norm has no mean
+    assert norm(x=None) == NULLPTR and norm(w=None) == NULLPTR and norm(y=None) == NULLPTR
+    assert norm(x=A16 + 1) == ALIGN and norm(y=A16 + 1) == ALIGN and norm(xd=FP32, x=A16 + 2) == ALIGN
+    assert norm(wd=FP32, w=A16 + 2) == ALIGN and norm(mean=A16 + 2) == ALIGN and norm(rstd=A16 + 1) == ALIGN
+    assert norm(ldx=255) == LD and norm(ldy=255) == LD
+    assert norm(C=16385, ldx=16385, ldy=16385) == UNSUP
+
+
+def quant(T=4, C=256, x=A16, ldx=256, q=A16, ldq=256, s=A16, kind=0, mean=None, rstd=None, w=A16, b=None, eps=1e-5):
+    return P.lib.puro_layer_norm_quant(kind, BF16, x, T, C, ldx, BF16, w, b, eps, q, ldq, s, mean, rstd, None)
+
+
+def test_norm_quant_refusals():
+    assert quant(T=0) == OK and quant(C=0) == OK
+    assert quant(C=200) == SHAPE and quant(T=-1) == SHAPE
+    assert quant(q=None) == NULLPTR and quant(s=None) == NULLPTR and quant(x=None) == NULLPTR
+    assert quant(x=MIS) == ALIGN and quant(q=MIS) == ALIGN and quant(s=MIS) == ALIGN and quant(w=MIS) == ALIGN
+    assert quant(b=MIS) == ALIGN
+    assert quant(ldx=128) == LD and quant(ldx=260) == LD and quant(ldq=264) == LD and quant(ldq=128) == LD
+    assert quant(kind=1, mean=A16) == ARG and quant(eps=-1.0) == ARG
+    assert quant(C=16512, ldx=16512, ldq=16512) == UNSUP
+
+
+def dual(T=256, C=256, q=A16, s=A16, qT=A16, ldqT=256, sT=A16, mean=A16, rstd=A16, kind=0, ldq=256):
+    return P.lib.puro_layer_norm_quant_dual(kind, BF16, A16, T, C, max(C, 1), BF16, A16, None, 1e-5, q, ldq, s, qT, ldqT, sT,
+                                            mean, rstd, None)
+
+
+def test_norm_quant_dual_refusals():
+    assert dual(T=0) == OK and dual(C=0) == OK
+    assert dual(T=100) == SHAPE and dual(C=64) == SHAPE and dual(T=-128) == SHAPE
+    for a in ("q", "s", "qT", "sT", "rstd", "mean"):
+        assert dual(**{a: None}) == NULLPTR, a
+    for a in ("q", "s", "qT", "sT"):
+        assert dual(**{a: MIS}) == ALIGN, a
+    assert dual(ldqT=128) == LD and dual(ldqT=264) == LD and dual(ldq=264) == LD
+    assert dual(kind=1) == ARG and dual(kind=1, mean=None, rstd=None) == NULLPTR
+
+
+def bwd(kind=0, T=64, C=256, dy=A16, x=A16, ld=256, w=A16, mean=A16, rstd=A16, dx=A16, dw=A16, db=A16, acc=0, ws=A16,
+        wb=1 << 30, xd=BF16, lddx=None):
+    return P.lib.puro_layer_norm_backward(kind, xd, dy, ld, x, ld, T, C, BF16, w, mean, rstd, dx,
+                                          ld if lddx is None else lddx, dw, db, acc, ws, wb, None)
+
+
+def test_norm_backward_refusals():
+    assert bwd(C=0) == OK and bwd(T=0, acc=1) == OK
+    assert bwd(kind=3) == MODE and bwd(xd=7) == DTYPE and bwd(T=-1) == SHAPE
+    assert bwd(acc=2) == ARG and bwd(kind=1) == ARG
+    for a in ("dy", "x", "w", "mean", "rstd", "dx", "dw"):
+        assert bwd(**{a: None}) == NULLPTR, a
+    assert bwd(x=A16 + 1) == ALIGN and bwd(dw=A16 + 2) == ALIGN and bwd(mean=A16 + 1) == ALIGN
+    assert bwd(ld=255) == LD and bwd(lddx=255) == LD
+    assert bwd(C=16385, ld=16385) == UNSUP
+    need = P.puro_layer_norm_backward_workspace_size(16384, 2048)
+    assert need > 0
+    assert bwd(T=16384, C=2048, ld=2048, wb=need - 1) == WORKSPACE and bwd(T=16384, C=2048, ld=2048, ws=None) == WORKSPACE
+    assert bwd(T=16384, C=2048, ld=2048, ws=MIS) == ALIGN
+    assert P.puro_layer_norm_backward_workspace_size(0, 2048) == 0
+    assert P.puro_layer_norm_backward_workspace_size(1, 2048) == 0
+    assert P.puro_layer_norm_backward_workspace_size(8, 1 << 20) == 0
+
+
+def jobs(*js):
+    return (P.GradJob * max(len(js), 1))(*[P.GradJob(*j) for j in js])
+
+
+def clip(js, n=None, max_norm=1.0, norm=A16, ws=A16, wb=1 << 20):
+    return P.lib.puro_clip_grad_norm(jobs(*js), len(js) if n is None else n, max_norm, norm, ws, wb, None)
+
+
+def test_clip_refusals():
+    good = (A16, A16, 100, FP32)
+    for m in (-1.0, math.nan):
+        assert clip([good], max_norm=m) == ARG
+        assert P.lib.puro_scale_by_norm(jobs(good), 1, m, A16, None) == ARG
+    assert clip([good], n=-1) == SHAPE and clip([(A16, A16, -1, FP32)]) == SHAPE
+    assert clip([(A16, A16, 100, 3)]) == DTYPE
+    assert clip([(None, A16, 100, FP32)]) == NULLPTR and clip([(A16, None, 100, FP32)]) == NULLPTR
+    assert clip([good], norm=None) == NULLPTR and clip([good], norm=A16 + 2) == ALIGN
+    assert clip([(A16 + 2, A16, 100, FP32)]) == ALIGN and clip([(A16 + 2, A16 + 1, 100, BF16)]) == ALIGN
+    assert clip([good], ws=None) == WORKSPACE and clip([good], wb=4) == WORKSPACE and clip([good], ws=MIS) == ALIGN
+    assert P.lib.puro_clip_grad_norm(None, 1, 1.0, A16, A16, 1 << 20, None) == NULLPTR
+    assert P.lib.puro_scale_by_norm(jobs(good), 1, 1.0, None, None) == NULLPTR
+
+
+def test_clip_refuses_overlaps():
+    B = A16 + 4096
+    same = (A16, A16, 100, FP32)
+    assert clip([same, same]) == ARG                                    # one gradient listed twice
+    assert clip([same, (A16 + 396, A16 + 396, 100, FP32)]) == ARG       # the last element is shared
+    assert clip([(A16, B, 100, FP32), (B + 396, B + 4096, 100, FP32)]) == ARG    # an output over another's input
+    assert clip([(A16, A16 + 4, 100, FP32)]) == ARG                     # an output shifted over its own input
+    # two inputs may overlap; side by side is fine: these calls get as far as the workspace
+    assert clip([(A16, B, 100, FP32), (A16, B + 400, 100, FP32)], ws=None) == WORKSPACE
+    assert clip([same, (A16 + 400, A16 + 400, 100, FP32)], ws=None) == WORKSPACE
+
+
+def test_grad_workspace_size():
+    size = P.lib.puro_grad_norm_workspace_size
+    assert size(jobs(), 0) == 0 and size(jobs((A16, None, 0, FP32)), 1) == 0
+    assert size(jobs((A16, None, 1, FP32)), 1) == 8
+    # 8192 fp32 elements make one step of a workgroup; one more needs a second, and so does a start off 16 bytes
+    assert size(jobs((A16, None, 8192, FP32)), 1) == 8 and size(jobs((A16, None, 8193, FP32)), 1) == 16
+    assert size(jobs((A16 + 4, None, 8192, FP32)), 1) == 16
+    assert size(jobs(*[(A16, None, 1, BF16)] * 300), 300) == 300 * 8
+    assert size(jobs((A16, None, 1, 9)), 1) == 0
+
+
+def rows(M=3, N=256, K=256, A=A16, lda=256, sA=A16, B=A16, ldb=256, sB=A16, C=A16, ldc=256, od=BF16, ws=None, wb=0):
+    return P.lib.puro_gemm_rows(M, N, K, A, lda, sA, B, ldb, sB, C, ldc, od, ws, wb, None)
+
+
+def test_rows_refusals():
+    assert rows(M=0) == OK and rows(N=0) == OK
+    assert rows(M=-1) == SHAPE and rows(N=200) == SHAPE and rows(K=100) == SHAPE
+    assert rows(od=2) == DTYPE
+    for a in ("A", "sA", "B", "sB", "C"):
+        assert rows(**{a: None}) == NULLPTR, a
+    for a in ("A", "B", "C"):
+        assert rows(**{a: MIS}) == ALIGN, a
+    assert rows(sA=A16 + 2) == ALIGN and rows(sB=A16 + 1) == ALIGN
+    assert rows(lda=128) == LD and rows(ldb=264) == LD and rows(ldc=128) == LD and rows(ldc=260) == LD
+    assert rows(M=1 << 32) == UNSUP
+    assert P.puro_gemm_rows_workspace_size(0, 128, 128) == 0 and P.puro_gemm_rows_workspace_size(-1, 128, 128) == 0
+
+
+def test_binding_refuses_what_the_library_cannot_see():
+    import torch
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    w = torch.ones(128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        P.puro_layer_norm(x, w)                                          # host tensors
+    with pytest.raises(TypeError):
+        P.puro_layer_norm(x.half(), w)
+    with pytest.raises(TypeError):
+        P.puro_clip_grad_norm([x.double()], 1.0)
+    with pytest.raises(ValueError):
+        P.puro_clip_grad_norm([x], 1.0, outs=[])
+    with pytest.raises(ValueError):
+        P.puro_scale_by_norm([], 1.0, None)
+    with pytest.raises(ValueError):
+        P.puro_gemm_rows(x, x, x, x)
+    with pytest.raises(ValueError):
+        P.puro_gemm_rows(x[0], x, x, x)
