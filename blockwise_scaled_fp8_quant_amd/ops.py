@@ -13,7 +13,7 @@ import functools
 
 import torch
 
-from . import OUT_BF16, OUT_FP32, PuroError, _check, _i64, _int, _need, _p, _stream, _sz, lib
+from . import OUT_BF16, OUT_FP32, _check, _i64, _int, _need, _p, _sz, lib
 
 __all__ = [
     "LAYER_NORM", "RMS_NORM", "EXPORTED_OPS", "GradJob", "puro_layer_norm", "puro_layer_norm_quant",
@@ -37,7 +37,7 @@ class GradJob(ctypes.Structure):
     _fields_ = [("src", _p), ("dst", _p), ("n", _i64), ("dtype", _int)]
 
 
-_jobs = ctypes.POINTER(GradJob)
+_jobs = _p     # a host array of GradJob
 _norm_in = [_int, _int, _p, _i64, _i64, _i64, _int, _p, _p, _f32]
 lib.puro_layer_norm.argtypes = _norm_in + [_p, _i64, _p, _p, _p]
 lib.puro_layer_norm_quant.argtypes = _norm_in + [_p, _i64, _p, _p, _p, _p]
@@ -55,6 +55,45 @@ for _f in EXPORTED_OPS:
     getattr(lib, _f).restype = _sz if _f.endswith("_workspace_size") else _int
 
 _DTYPE = {torch.bfloat16: OUT_BF16, torch.float32: OUT_FP32}
+_f32t, _u8t = torch.float32, torch.uint8
+_raw_stream = torch._C._cuda_getCurrentRawStream    # the current stream's handle, without the wrapper's checks
+
+
+def _device() -> int:
+    """The current GPU's index; one that no tensor has where there is no GPU (every check then refuses)."""
+    try:
+        return torch._C._cuda_getDevice()
+    except RuntimeError:
+        return -2
+
+
+# The checks below are the package's (_need), with the passing case first: a decode step calls these entry points
+# thousands of times a second, and its time is the host's.  (Two further differences: a dimension of one element may
+# carry any stride, as in is_contiguous, and rows may be any distance apart that is no less than their length.)
+def _whole(t, what: str, dtype, shape, dev: int) -> int:
+    """Data pointer of a contiguous tensor of `dtype` (None: any) and `shape` (None: any) on GPU `dev`."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and (dtype is None or t.dtype is dtype)
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, what, getattr(t, "dtype", None) if dtype is None else dtype, shape, whole=True)
+    raise ValueError(f"{what}: must be contiguous")
+
+
+def _rows_of(t, what: str, dtype, shape, dev: int) -> int:
+    """Row stride of a matrix of `dtype` and `shape` (None: any two dimensions) on GPU `dev`."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{what}: expected a 2-D tensor")
+    T, C = t.shape
+    if t.get_device() != dev or t.dtype is not dtype or (shape is not None and t.shape != shape):
+        _need(t, what, dtype, shape)
+    ld, step = t.stride()
+    if step != 1 and C > 1 and T > 0:
+        raise ValueError(f"{what}: rows must have unit element stride (got strides {t.stride()})")
+    if T <= 1 or C == 0:
+        return C if C > 0 else 1                    # a single row's stride says nothing
+    if ld < C:
+        raise ValueError(f"{what}: row stride {ld} is smaller than a row of {C}")
+    return ld
 
 
 def _dtype(t, what: str) -> int:
@@ -70,63 +109,58 @@ def _kind(kind) -> int:
     return kind
 
 
-def _matrix(x, what: str):
-    """(rows, columns, row stride) of a bf16 or fp32 matrix on the current GPU with unit element stride."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError(f"{what}: expected a 2-D tensor")
-    _need(x, what, x.dtype, None)
-    T, C = x.shape
-    return T, C, _row_stride(x)
-
-
-def _row_stride(t) -> int:
-    """Row stride of a checked matrix; a single row or an empty one may carry any stride."""
-    T, C = t.shape
-    if T <= 1:
-        return max(C, 1)
-    if t.stride(0) < C:
-        raise ValueError(f"row stride {t.stride(0)} is smaller than a row of {C}")
-    return t.stride(0)
-
-
-def _vector(v, what: str, C: int):
-    _need(v, what, v.dtype if isinstance(v, torch.Tensor) else None, (C,), whole=True)
-    return v.data_ptr()
-
-
-def _norm_inputs(x, weight, bias, eps, kind):
+def _norm_inputs(x, weight, bias, eps, kind, dev):
     """Checks and C arguments that every forward form shares."""
     xd = _dtype(x, "x")
-    T, C, ldx = _matrix(x, "x")
+    ldx = _rows_of(x, "x", x.dtype, None, dev)
+    T, C = x.shape
     wd = _dtype(weight, "weight")
-    pw = _vector(weight, "weight", C)
-    pb = None
-    if bias is not None:
-        if _dtype(bias, "bias") != wd:
-            raise TypeError(f"bias: dtype {bias.dtype}, expected the weight's {weight.dtype}")
-        pb = _vector(bias, "bias", C)
-    return T, C, [_kind(kind), xd, x.data_ptr(), T, C, ldx, wd, pw, pb, eps]
+    pw = _whole(weight, "weight", weight.dtype, (C,), dev)
+    pb = None if bias is None else _whole(bias, "bias", weight.dtype, (C,), dev)
+    return T, C, (_kind(kind), xd, x.data_ptr(), T, C, ldx, wd, pw, pb, eps)
 
 
-def _stats(x, T, mean, rstd, kind, make):
-    """The statistics' tensors: allocated where wanted and not given, checked where given."""
-    if kind == RMS_NORM:
-        if mean is not None:
+def _stats(T, mean, rstd, kind, make, dev):
+    """The statistics' tensors (allocated where wanted and not given) and their pointers."""
+    pm = pr = None
+    if mean is not None:
+        if kind == RMS_NORM:
             raise ValueError("mean: an RMS norm has none")
-    elif mean is None and make:
-        mean = torch.empty(T, dtype=torch.float32, device=x.device)
-    elif mean is not None:
-        _need(mean, "mean", torch.float32, (T,), whole=True)
-    if rstd is None:
-        if make:
-            rstd = torch.empty(T, dtype=torch.float32, device=x.device)
-    else:
-        _need(rstd, "rstd", torch.float32, (T,), whole=True)
-    return mean, rstd
+        pm = _whole(mean, "mean", _f32t, (T,), dev)
+    elif make and kind == LAYER_NORM:
+        mean = torch.empty(T, dtype=_f32t, device="cuda")
+        pm = mean.data_ptr()
+    if rstd is not None:
+        pr = _whole(rstd, "rstd", _f32t, (T,), dev)
+    elif make:
+        rstd = torch.empty(T, dtype=_f32t, device="cuda")
+        pr = rstd.data_ptr()
+    return mean, rstd, pm, pr
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _out_rows(t, what, dtype, shape, dev):
+    """An output matrix and its row stride."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device="cuda"), shape[1] or 1
+    return t, _rows_of(t, what, dtype, shape, dev)
+
+
+def _out_whole(t, what, dtype, shape, dev):
+    """A contiguous output and its pointer."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device="cuda")
+        return t, t.data_ptr()
+    return t, _whole(t, what, dtype, shape, dev)
+
+
+def _workspace(workspace, need: int, dev):
+    """(workspace, its pointer, its bytes): allocated when needed and not given."""
+    if workspace is None:
+        if not need:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=_u8t, device="cuda")
+        return workspace, workspace.data_ptr(), need
+    return workspace, _whole(workspace, "workspace", None, None, dev), workspace.numel() * workspace.element_size()
 
 
 def _on_stream(call):
@@ -142,23 +176,17 @@ def _on_stream(call):
     return entry
 
 
-def _out(t, what, x, dtype, shape, whole=False):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=x.device)
-    return _need(t, what, dtype, shape, whole)
-
-
 @_on_stream
 def puro_layer_norm(x, weight, bias=None, eps: float = 1e-5, kind: int = LAYER_NORM, y=None, mean=None, rstd=None,
                     stats: bool = True):
     """x [T, C] bf16 or fp32 -> (y [T, C] of x's type, mean fp32 [T], rstd fp32 [T]): the layer or RMS norm
     of each row and the statistics its backward pass takes.  mean is None for RMS_NORM; with stats=False
     only the statistics given are written.  y may be x."""
-    T, C, args = _norm_inputs(x, weight, bias, eps, kind)
-    y = _out(y, "y", x, x.dtype, (T, C))
-    mean, rstd = _stats(x, T, mean, rstd, kind, stats)
-    _check(lib.puro_layer_norm(*args, y.data_ptr(), _row_stride(y), _ptr(mean), _ptr(rstd), _stream(None)),
-           "puro_layer_norm")
+    dev = _device()
+    T, C, args = _norm_inputs(x, weight, bias, eps, kind, dev)
+    y, ldy = _out_rows(y, "y", x.dtype, (T, C), dev)
+    mean, rstd, pm, pr = _stats(T, mean, rstd, kind, stats, dev)
+    _check(lib.puro_layer_norm(*args, y.data_ptr(), ldy, pm, pr, _raw_stream(dev)), "puro_layer_norm")
     return y, mean, rstd
 
 
@@ -167,12 +195,12 @@ def puro_layer_norm_quant(x, weight, bias=None, eps: float = 1e-5, kind: int = L
                           rstd=None):
     """x [T, C] -> (q uint8 [T, C], s fp32 [C/128, T]): the norm of each row as 1x128 codes and scales
     (layouts of puro_fp8_quant_act_1x128), for any T.  mean and rstd are written where given."""
-    T, C, args = _norm_inputs(x, weight, bias, eps, kind)
-    q = _out(q, "q", x, torch.uint8, (T, C))
-    s = _out(s, "s", x, torch.float32, (C // 128, T), True)
-    mean, rstd = _stats(x, T, mean, rstd, kind, False)
-    _check(lib.puro_layer_norm_quant(*args, q.data_ptr(), _row_stride(q), s.data_ptr(), _ptr(mean), _ptr(rstd),
-                                     _stream(None)), "puro_layer_norm_quant")
+    dev = _device()
+    T, C, args = _norm_inputs(x, weight, bias, eps, kind, dev)
+    q, ldq = _out_rows(q, "q", _u8t, (T, C), dev)
+    s, ps = _out_whole(s, "s", _f32t, (C // 128, T), dev)
+    _, _, pm, pr = _stats(T, mean, rstd, kind, False, dev)
+    _check(lib.puro_layer_norm_quant(*args, q.data_ptr(), ldq, ps, pm, pr, _raw_stream(dev)), "puro_layer_norm_quant")
     return q, s
 
 
@@ -181,31 +209,20 @@ def puro_layer_norm_quant_dual(x, weight, bias=None, eps: float = 1e-5, kind: in
                                sT=None, mean=None, rstd=None):
     """x [T, C] -> (q [T, C], s [C/128, T], qT [C, T], sT [T/128, C], mean, rstd): the norm of each row as the
     codes and scales of both orientations (layouts of puro_fp8_quant_act_dual), and its statistics."""
-    T, C, args = _norm_inputs(x, weight, bias, eps, kind)
-    q = _out(q, "q", x, torch.uint8, (T, C))
-    s = _out(s, "s", x, torch.float32, (C // 128, T), True)
-    qT = _out(qT, "qT", x, torch.uint8, (C, T))
-    sT = _out(sT, "sT", x, torch.float32, (T // 128, C), True)
-    mean, rstd = _stats(x, T, mean, rstd, kind, True)
-    _check(lib.puro_layer_norm_quant_dual(*args, q.data_ptr(), _row_stride(q), s.data_ptr(), qT.data_ptr(),
-                                          _row_stride(qT), sT.data_ptr(), _ptr(mean), _ptr(rstd), _stream(None)),
-           "puro_layer_norm_quant_dual")
+    dev = _device()
+    T, C, args = _norm_inputs(x, weight, bias, eps, kind, dev)
+    q, ldq = _out_rows(q, "q", _u8t, (T, C), dev)
+    s, ps = _out_whole(s, "s", _f32t, (C // 128, T), dev)
+    qT, ldqT = _out_rows(qT, "qT", _u8t, (C, T), dev)
+    sT, psT = _out_whole(sT, "sT", _f32t, (T // 128, C), dev)
+    mean, rstd, pm, pr = _stats(T, mean, rstd, kind, True, dev)
+    _check(lib.puro_layer_norm_quant_dual(*args, q.data_ptr(), ldq, ps, qT.data_ptr(), ldqT, psT, pm, pr,
+                                          _raw_stream(dev)), "puro_layer_norm_quant_dual")
     return q, s, qT, sT, mean, rstd
 
 
 def puro_layer_norm_backward_workspace_size(T: int, C: int) -> int:
     return lib.puro_layer_norm_backward_workspace_size(T, C)
-
-
-def _workspace(workspace, need: int, device):
-    """(workspace, its bytes): allocated when needed and not given."""
-    if workspace is None:
-        if not need:
-            return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    else:
-        _need(workspace, "workspace", workspace.dtype if isinstance(workspace, torch.Tensor) else None, None, whole=True)
-    return workspace, workspace.numel() * workspace.element_size()
 
 
 @_on_stream
@@ -214,50 +231,61 @@ def puro_layer_norm_backward(dy, x, weight, mean, rstd, kind: int = LAYER_NORM, 
     """(dx [T, C] of x's type, dweight fp32 [C], dbias fp32 [C] or None): the backward pass of the norm, from
     the statistics of the forward pass (mean is None for RMS_NORM).  accumulate adds to the dweight and dbias given.
     dx may be dy or x."""
+    dev = _device()
     xd = _dtype(x, "x")
-    T, C, ldx = _matrix(x, "x")
-    _need(dy, "dy", x.dtype, (T, C))
+    ldx = _rows_of(x, "x", x.dtype, None, dev)
+    T, C = x.shape
+    lddy = _rows_of(dy, "dy", x.dtype, (T, C), dev)
     wd = _dtype(weight, "weight")
-    pw = _vector(weight, "weight", C)
+    pw = _whole(weight, "weight", weight.dtype, (C,), dev)
+    pm = None
     if _kind(kind) == LAYER_NORM:
-        _need(mean, "mean", torch.float32, (T,), whole=True)
+        pm = _whole(mean, "mean", _f32t, (T,), dev)
     elif mean is not None:
         raise ValueError("mean: an RMS norm has none")
-    _need(rstd, "rstd", torch.float32, (T,), whole=True)
+    pr = _whole(rstd, "rstd", _f32t, (T,), dev)
     if accumulate and (dweight is None or (with_bias and dbias is None)):
         raise ValueError("accumulate: needs the gradients it adds to")
-    dx = _out(dx, "dx", x, x.dtype, (T, C))
-    dweight = _out(dweight, "dweight", x, torch.float32, (C,), True)
+    dx, lddx = _out_rows(dx, "dx", x.dtype, (T, C), dev)
+    dweight, pdw = _out_whole(dweight, "dweight", _f32t, (C,), dev)
+    pdb = None
     if with_bias or dbias is not None:
-        dbias = _out(dbias, "dbias", x, torch.float32, (C,), True)
-    workspace, wbytes = _workspace(workspace, lib.puro_layer_norm_backward_workspace_size(T, C), x.device)
-    _check(lib.puro_layer_norm_backward(kind, xd, dy.data_ptr(), _row_stride(dy), x.data_ptr(), ldx, T, C, wd, pw,
-                                        _ptr(mean), rstd.data_ptr(), dx.data_ptr(), _row_stride(dx), dweight.data_ptr(),
-                                        _ptr(dbias), 1 if accumulate else 0, _ptr(workspace), wbytes,
-                                        _stream(None)), "puro_layer_norm_backward")
+        dbias, pdb = _out_whole(dbias, "dbias", _f32t, (C,), dev)
+    workspace, pws, wbytes = _workspace(workspace, lib.puro_layer_norm_backward_workspace_size(T, C), dev)
+    _check(lib.puro_layer_norm_backward(kind, xd, dy.data_ptr(), lddy, x.data_ptr(), ldx, T, C, wd, pw, pm, pr,
+                                        dx.data_ptr(), lddx, pdw, pdb, 1 if accumulate else 0, pws, wbytes,
+                                        _raw_stream(dev)), "puro_layer_norm_backward")
     return dx, dweight, dbias
 
 
-def _grad_jobs(grads, outs):
-    """The job array of a list of gradients, and the device they share."""
+def _grad_jobs(grads, outs, dev):
+    """The job array (puro_grad_job) of a list of gradients: four 64-bit words each."""
+    words = []
     if outs is not None and len(outs) != len(grads):
         raise ValueError(f"outs: {len(outs)} tensors for {len(grads)} gradients")
-    jobs = (GradJob * max(len(grads), 1))()
     for i, g in enumerate(grads):
-        code = _dtype(g, f"grads[{i}]")
-        _need(g, f"grads[{i}]", g.dtype, None, whole=True)
+        dtype = getattr(g, "dtype", None)
+        code = _DTYPE.get(dtype)
+        if code is None:
+            _dtype(g, f"grads[{i}]")
+        # (the tests of _whole, inline: a model has hundreds of gradients)
+        if g.get_device() != dev or not g.is_contiguous():
+            _whole(g, f"grads[{i}]", dtype, None, dev)
         src = dst = g.data_ptr()
         if outs is not None:
-            dst = _need(outs[i], f"outs[{i}]", g.dtype, g.shape, whole=True).data_ptr()
-        job = jobs[i]
-        job.src, job.dst, job.n, job.dtype = src, dst, g.numel(), code
-    return jobs
+            o = outs[i]
+            if not (isinstance(o, torch.Tensor) and o.dtype is dtype and o.get_device() == dev and o.shape == g.shape
+                    and o.is_contiguous()):
+                _whole(o, f"outs[{i}]", dtype, g.shape, dev)
+            dst = o.data_ptr()
+        words += (src, dst, g.numel(), code)
+    return (_i64 * max(len(words), 4))(*words)
 
 
-def _norm_tensor(norm):
+def _norm_tensor(norm, dev):
     if norm is None:
-        return torch.empty((), dtype=torch.float32, device="cuda")
-    _need(norm, "norm", torch.float32, None, whole=True)
+        return torch.empty((), dtype=_f32t, device="cuda")
+    _whole(norm, "norm", _f32t, None, dev)
     if norm.numel() != 1:
         raise ValueError("norm: expected one value")
     return norm
@@ -267,12 +295,12 @@ def _norm_tensor(norm):
 def puro_grad_norm(grads, norm=None, workspace=None):
     """norm (fp32, one value, on the GPU): the square root of the sum of all squares of a list of contiguous
     bf16 or fp32 tensors."""
+    dev = _device()
     grads = list(grads)
-    jobs = _grad_jobs(grads, None)
-    norm = _norm_tensor(norm)
-    workspace, wbytes = _workspace(workspace, lib.puro_grad_norm_workspace_size(jobs, len(grads)), norm.device)
-    _check(lib.puro_grad_norm(jobs, len(grads), norm.data_ptr(), _ptr(workspace), wbytes, _stream(None)),
-           "puro_grad_norm")
+    jobs = _grad_jobs(grads, None, dev)
+    norm = _norm_tensor(norm, dev)
+    workspace, pws, wbytes = _workspace(workspace, lib.puro_grad_norm_workspace_size(jobs, len(grads)), dev)
+    _check(lib.puro_grad_norm(jobs, len(grads), norm.data_ptr(), pws, wbytes, _raw_stream(dev)), "puro_grad_norm")
     return norm
 
 
@@ -280,12 +308,13 @@ def puro_grad_norm(grads, norm=None, workspace=None):
 def puro_clip_grad_norm(grads, max_norm: float, outs=None, norm=None, workspace=None):
     """(norm, outs): the global norm of a list of contiguous bf16 or fp32 tensors, and the tensors times
     min(1, max_norm / (norm + 1e-6)) -- in place (outs is then grads), or into the tensors given as outs."""
+    dev = _device()
     grads = list(grads)
-    jobs = _grad_jobs(grads, outs)
-    norm = _norm_tensor(norm)
-    workspace, wbytes = _workspace(workspace, lib.puro_grad_norm_workspace_size(jobs, len(grads)), norm.device)
-    _check(lib.puro_clip_grad_norm(jobs, len(grads), max_norm, norm.data_ptr(), _ptr(workspace), wbytes,
-                                   _stream(None)), "puro_clip_grad_norm")
+    jobs = _grad_jobs(grads, outs, dev)
+    norm = _norm_tensor(norm, dev)
+    workspace, pws, wbytes = _workspace(workspace, lib.puro_grad_norm_workspace_size(jobs, len(grads)), dev)
+    _check(lib.puro_clip_grad_norm(jobs, len(grads), max_norm, norm.data_ptr(), pws, wbytes, _raw_stream(dev)),
+           "puro_clip_grad_norm")
     return norm, grads if outs is None else outs
 
 
@@ -293,12 +322,13 @@ def puro_clip_grad_norm(grads, max_norm: float, outs=None, norm=None, workspace=
 def puro_scale_by_norm(grads, max_norm: float, norm, outs=None):
     """The tensors times min(1, max_norm / (norm + 1e-6)) with a norm already on the GPU (for instance joined
     over processes); in place, or into outs.  Returns the tensors written."""
-    grads = list(grads)
-    jobs = _grad_jobs(grads, outs)
     if norm is None:
         raise ValueError("norm: the scaling needs the norm's tensor")
-    norm = _norm_tensor(norm)
-    _check(lib.puro_scale_by_norm(jobs, len(grads), max_norm, norm.data_ptr(), _stream(None)), "puro_scale_by_norm")
+    dev = _device()
+    grads = list(grads)
+    jobs = _grad_jobs(grads, outs, dev)
+    norm = _norm_tensor(norm, dev)
+    _check(lib.puro_scale_by_norm(jobs, len(grads), max_norm, norm.data_ptr(), _raw_stream(dev)), "puro_scale_by_norm")
     return grads if outs is None else outs
 
 
@@ -310,22 +340,19 @@ def puro_gemm_rows_workspace_size(M: int, N: int, K: int) -> int:
 def puro_gemm_rows(A, sA, B, sB, C=None, out_dtype: int = OUT_BF16, workspace=None):
     """C [M, N] = blockwise-scaled FP8 product of A [M, K] (sA fp32 [K/128, M]) and B [N, K] (sB fp32
     [N/128, K/128]) for any number of rows M; see puro_ops.h."""
-    for t, what in ((A, "A"), (B, "B")):
-        if not isinstance(t, torch.Tensor) or t.dim() != 2:
-            raise ValueError(f"{what}: expected a 2-D tensor")
+    dev = _device()
+    lda = _rows_of(A, "A", _u8t, None, dev)
+    ldb = _rows_of(B, "B", _u8t, None, dev)
     M, K = A.shape
     N, KB = B.shape
     if KB != K:
         raise ValueError(f"A [{M}, {K}] and B [{N}, {KB}] differ in the contraction length")
-    _need(A, "A", torch.uint8, None)
-    _need(B, "B", torch.uint8, None)
-    _need(sA, "sA", torch.float32, (K // 128, M), whole=True)
-    _need(sB, "sB", torch.float32, (N // 128, K // 128), whole=True)
+    psA = _whole(sA, "sA", _f32t, (K // 128, M), dev)
+    psB = _whole(sB, "sB", _f32t, (N // 128, K // 128), dev)
     if out_dtype not in (OUT_BF16, OUT_FP32):
         raise ValueError(f"out_dtype {out_dtype}: expected OUT_BF16 or OUT_FP32")
-    C = _out(C, "C", A, torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32, (M, N))
-    workspace, wbytes = _workspace(workspace, lib.puro_gemm_rows_workspace_size(M, N, K), A.device)
-    _check(lib.puro_gemm_rows(M, N, K, A.data_ptr(), _row_stride(A), sA.data_ptr(), B.data_ptr(), _row_stride(B),
-                              sB.data_ptr(), C.data_ptr(), _row_stride(C), out_dtype, _ptr(workspace), wbytes,
-                              _stream(None)), "puro_gemm_rows")
+    C, ldc = _out_rows(C, "C", torch.bfloat16 if out_dtype == OUT_BF16 else _f32t, (M, N), dev)
+    workspace, pws, wbytes = _workspace(workspace, lib.puro_gemm_rows_workspace_size(M, N, K), dev)
+    _check(lib.puro_gemm_rows(M, N, K, A.data_ptr(), lda, psA, B.data_ptr(), ldb, psB, C.data_ptr(), ldc, out_dtype, pws,
+                              wbytes, _raw_stream(dev)), "puro_gemm_rows")
     return C

@@ -116,6 +116,10 @@ def test_refusals(P):
         P.puro_clip_grad_norm([g], 1.0, outs=[t.ones(64, device="cuda")])
     with pytest.raises(TypeError):
         P.puro_clip_grad_norm([g], 1.0, outs=[g.bfloat16()])
+    with pytest.raises(TypeError):
+        P.puro_clip_grad_norm([g], 1.0, outs=[None])
+    with pytest.raises(ValueError):
+        P.puro_clip_grad_norm([g.cpu()], 1.0)
     with pytest.raises(P.PuroError):
         P.puro_clip_grad_norm([g, g], 1.0)
     with pytest.raises(P.PuroError):

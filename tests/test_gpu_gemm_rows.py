@@ -74,6 +74,18 @@ def test_strides_and_gaps(P):
         assert (C == 5).all()
 
 
+def test_single_row_and_column_views(P):
+    """Dimensions of one element may carry any stride: one row's scales are a column however they were made."""
+    t = torch()
+    A, sA, B, sB = operands(1, 128, 512, 4)
+    want = P.puro_gemm_rows(A, sA, B, sB)
+    odd = sA.t().contiguous().t()
+    assert odd.shape == sA.shape and t.equal(P.puro_gemm_rows(A.expand(1, 512), odd, B, sB), want)
+    wide = t.zeros((3, 512), dtype=t.uint8, device="cuda")
+    wide[1] = A[0]
+    assert t.equal(P.puro_gemm_rows(wide[1:2], sA, B, sB), want)
+
+
 def test_exact_integers(P):
     """Small integers with power-of-two scales: every partial sum is exact, so the result is."""
     t = torch()
