@@ -78,13 +78,24 @@ __device__ __forceinline__ void unpack8(const Raw8<BF16>& r, float v[8]) {
   }
 }
 
-template <bool BF16, bool VEC>
+// NT: past the caches.  Measured at 16384 x 2048 bf16 with inputs in rotation: the forward pass 23.2 us with
+// such stores and 25.4 without (they leave the memory-side cache to x), the backward pass 42.0 and 38.9 (its
+// inputs exceed that cache).
+template <bool NT, typename V>
+__device__ __forceinline__ void put(V v, V* p) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+
+template <bool BF16, bool VEC, bool NT>
 __device__ __forceinline__ void store8(void* base, int64_t at, int nv, const float v[8]) {
   if constexpr (BF16) {
     const u32x4 o = {bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
     uint16_t* p = static_cast<uint16_t*>(base) + at;
     if constexpr (VEC) {
-      if (nv > 0) __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(p));
+      if (nv > 0) put<NT>(o, reinterpret_cast<u32x4*>(p));
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -94,8 +105,8 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int nv, const flo
     float* p = static_cast<float*>(base) + at;
     if constexpr (VEC) {
       if (nv > 0) {
-        __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
-        __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(p + 4));
+        put<NT>(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
+        put<NT>(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(p + 4));
       }
     } else {
 #pragma unroll
@@ -105,8 +116,16 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int nv, const flo
   }
 }
 
-// Eight values of a weight or bias vector (read once per thread and launch; any alignment).
-__device__ __forceinline__ void load_vec8(const void* base, bool bf16, int col, int nv, float v[8]) {
+// Eight values of a weight or bias vector, read once per thread and launch: two 16-byte loads (one for
+// bf16) where the vector is aligned and all eight exist, else element by element.
+__device__ __forceinline__ void load_vec8(const void* base, bool bf16, bool aligned, int col, int nv, float v[8]) {
+  if (aligned && nv == 8) {
+    if (bf16)
+      unpack8<true>(load8<true, true>(base, col, 8), v);
+    else
+      unpack8<false>(load8<false, true>(base, col, 8), v);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     v[j] = 0.f;
@@ -115,6 +134,8 @@ __device__ __forceinline__ void load_vec8(const void* base, bool bf16, int col, 
                   : static_cast<const float*>(base)[col + j];
   }
 }
+
+__device__ __forceinline__ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // ---- sums over the lanes of a wave and the waves of a team -------------------------------------------
 template <int CTRL>
@@ -148,11 +169,37 @@ __device__ __forceinline__ float team_sum(float v, float (*red)[WAVES], int slot
   return v;
 }
 
-// scale and multiplier of a group from the bits of its fp32 maximum (sign cleared), as tile_scale
-__device__ __forceinline__ void tile_scale32(uint32_t amax_bits, float& s, float& r) {
-  const float a = __uint_as_float(umax(amax_bits, kAmaxFloorBf16 << 16));
+// Scale and multiplier of a group from its fp32 maximum, as tile_scale (codec.hpp).
+__device__ __forceinline__ void tile_scale32(float amax, float& s, float& r) {
+  const float a = __builtin_fmaxf(amax, __uint_as_float(kAmaxFloorBf16 << 16));
   s = a / kE4M3Max;
   r = kE4M3Max / a;
+}
+
+// The norm of eight columns for the quantized forms: two FMAs per element, (x r - mu r) g + b, with
+// shift = -mu r.  (The tensor form subtracts the mean first: one rounding less where |mu| is many deviations.
+// Three bits of mantissa do not show it, and the dual form's second launch is bound by its vector instructions.)
+template <bool BF16>
+__device__ __forceinline__ void norm8(const Raw8<BF16>& raw, float rstd, float shift, const float g[8], const float b[8],
+                                      float y[8]) {
+  unpack8<BF16>(raw, y);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(__builtin_fmaf(y[j], rstd, shift), g[j], b[j]);
+}
+
+// max(m, |a|, |b|): one v_max3_f32.  A NaN does not enter (its code is NaN whatever the scale).
+__device__ __forceinline__ float max3abs(float m, float a, float b) {
+  return __builtin_fmaxf(__builtin_fmaxf(m, __builtin_fabsf(a)), __builtin_fabsf(b));
+}
+
+// Four values to codes.  The convert that writes the low half keeps the other half of its register: one of
+// its own operands serves, where a zero would have to be put there first.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  return cvt2_hi(c, d, cvt2_lo(a, b, __float_as_uint(a)));
+}
+
+__device__ __forceinline__ float row16_maxf(float v) {   // v >= 0
+  return __uint_as_float(row16_max(__float_as_uint(v)));
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -176,26 +223,32 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs
 
   int col[ITER], nv[ITER];
   float g[ITER][8], b[ITER][8];
+  Raw8<BF16> next[ITER];
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
     col[i] = 8 * (kTeamThreads * i + tt);
     nv[i] = a.C - col[i] < 0 ? 0 : (a.C - col[i] > 8 ? 8 : a.C - col[i]);
+    next[i] = load8<BF16, VEC>(a.x, row0 * a.ldx + col[i], row0 < a.T ? nv[i] : 0);
+  }
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
     if constexpr (WHAT != 2) {
-      load_vec8(a.gamma, a.w_bf16, col[i], nv[i], g[i]);
-      load_vec8(a.beta, a.w_bf16, col[i], a.beta ? nv[i] : 0, b[i]);
+      load_vec8(a.gamma, a.w_bf16, aligned16(a.gamma), col[i], nv[i], g[i]);
+      load_vec8(a.beta, a.w_bf16, aligned16(a.beta), col[i], a.beta ? nv[i] : 0, b[i]);
     }
   }
   const float inv_c = 1.0f / (float)a.C;
-  Raw8<BF16> next[ITER];
-#pragma unroll
-  for (int i = 0; i < ITER; ++i) next[i] = load8<BF16, VEC>(a.x, row0 * a.ldx + col[i], row0 < a.T ? nv[i] : 0);
 
   for (int k = 0; k < a.rows_per_team; ++k) {
     const int64_t row = row0 + k;
     const bool ok = row < a.T;
     float v[ITER][8];
+    Raw8<BF16> cur[ITER];
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) unpack8<BF16>(next[i], v[i]);
+    for (int i = 0; i < ITER; ++i) {
+      cur[i] = next[i];
+      unpack8<BF16>(cur[i], v[i]);
+    }
     if (k + 1 < a.rows_per_team) {
 #pragma unroll
       for (int i = 0; i < ITER; ++i)
@@ -233,18 +286,19 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
         float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(v[i][j] * rstd, g[i][j], b[i][j]);
         if constexpr (WHAT == 0) {
-          store8<BF16, VEC>(a.y, row * a.ldy + col[i], ok ? nv[i] : 0, y);
-        } else {
-          uint32_t m = 0u;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) m = umax(m, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+          for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(v[i][j] * rstd, g[i][j], b[i][j]);
+          store8<BF16, VEC, true>(a.y, row * a.ldy + col[i], ok ? nv[i] : 0, y);
+        } else {
+          norm8<BF16>(cur[i], rstd, -mean * rstd, g[i], b[i], y);
+          float m = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) m = max3abs(m, y[j], y[j + 1]);
           float sc, r;
-          tile_scale32(row16_max(m), sc, r);
+          tile_scale32(row16_maxf(m), sc, r);
           if (ok && nv[i] > 0) {
-            const u32x2 o = {cvt4(y[0] * r, y[1] * r, y[2] * r, y[3] * r), cvt4(y[4] * r, y[5] * r, y[6] * r, y[7] * r)};
+            const u32x2 o = {codes4(y[0] * r, y[1] * r, y[2] * r, y[3] * r), codes4(y[4] * r, y[5] * r, y[6] * r, y[7] * r)};
             __builtin_nontemporal_store(o, reinterpret_cast<u32x2*>(a.q + row * a.ldq + col[i]));
             if ((tt & 15) == 0) a.s[(int64_t)(col[i] >> 7) * a.T + row] = sc;
           }
@@ -257,54 +311,61 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs
 // ---------------------------------------------------------------------------------------------------
 // Second launch of the dual form: a 128-row x 128-column tile per workgroup, as quant_dual_kernel
 // (quant.hip) on the norm formed in registers from x and the statistics of the first launch.  x is
-// read twice (once per launch); keeping 128 whole rows on one CU for a single read does not fit
+// read twice (once per launch): keeping 128 whole rows on one CU for a single read does not fit
 // beyond a few hundred columns.
+// Measured at 16384 x 2048 bf16: 23.5 us (5.6 TB/s of reads and writes together, as a copy).  It was bound by
+// vector instructions first (18 us with neither loads nor stores): the two-FMA norm, three-operand maxima on
+// magnitudes and converts without a register to clear took it from 27.6 us.
 // ---------------------------------------------------------------------------------------------------
+constexpr int kDualThreads = 256;
+
 template <bool BF16>
-__global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a, int bt) {
-  __shared__ uint32_t rowmax[128];
-  __shared__ uint32_t colred[4][128];
+__global__ __launch_bounds__(kDualThreads) void norm_dual_kernel(NormArgs a, int bt_log2) {
+  constexpr int kWaves = kDualThreads / 64;
+  constexpr int kRows = 128 * 16 / kDualThreads;   // tokens per thread: 8 (x 8 columns)
+  __shared__ float rowmax[128];
+  __shared__ float colred[kWaves][128];
   __shared__ float rrow[128], rcol[128];
   __shared__ uint32_t stage[128 * 33];
 
   const int t = threadIdx.x;
   const int lane = t & 63, wave = t >> 6;
   const int tc = t & 15, tr = t >> 4;
-  const int64_t b = blockIdx.x;
-  const int64_t run = b / bt, ncb = a.C / 128;
-  const int64_t tb = (run / ncb) * bt + (b - run * bt);
-  const int64_t gcol = run % ncb;
-  const int64_t tok0 = tb * 128 + tr * 8;
+  // tile order of tile_order (quant.hip), in 32 bits: runs of 2^bt_log2 token blocks of one column block
+  const uint32_t run = blockIdx.x >> bt_log2, ncb = (uint32_t)a.C / 128u;
+  const uint32_t run_row = run / ncb;
+  const int64_t tb = ((int64_t)run_row << bt_log2) + (blockIdx.x & ((1u << bt_log2) - 1u));
+  const int64_t gcol = run - run_row * ncb;
+  const int64_t tok0 = tb * 128 + tr * kRows;
   const int col0 = (int)gcol * 128 + tc * 8;
 
-  Raw8<BF16> raw[8];
+  Raw8<BF16> raw[kRows];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) raw[i] = load8<BF16, true>(a.x, (tok0 + i) * a.ldx + col0, 8);
+  for (int i = 0; i < kRows; ++i) raw[i] = load8<BF16, true>(a.x, (tok0 + i) * a.ldx + col0, 8);
   float g[8], be[8];
-  load_vec8(a.gamma, a.w_bf16, col0, 8, g);
-  load_vec8(a.beta, a.w_bf16, col0, a.beta ? 8 : 0, be);
+  load_vec8(a.gamma, a.w_bf16, true, col0, 8, g);
+  load_vec8(a.beta, a.w_bf16, true, col0, a.beta ? 8 : 0, be);
 
-  float y[8][8];
-  uint32_t cm[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+  float y[kRows][8];
+  float cm[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float mean = a.layer ? a.mean[tok0 + i] : 0.f, rstd = a.rstd[tok0 + i];
-    unpack8<BF16>(raw[i], y[i]);
-    uint32_t m = 0u;
+  for (int i = 0; i < kRows; ++i) {
+    const float rstd = a.rstd[tok0 + i], shift = a.layer ? -a.mean[tok0 + i] * rstd : 0.f;
+    norm8<BF16>(raw[i], rstd, shift, g, be, y[i]);
+    float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      y[i][j] = __builtin_fmaf((y[i][j] - mean) * rstd, g[j], be[j]);
-      const uint32_t bits = __float_as_uint(y[i][j]) & 0x7FFFFFFFu;
-      m = umax(m, bits);
-      cm[j] = umax(cm[j], bits);
-    }
-    m = row16_max(m);
-    if (tc == 0) rowmax[tr * 8 + i] = m;
+    for (int j = 0; j < 8; j += 2) m = max3abs(m, y[i][j], y[i][j + 1]);
+    m = row16_maxf(m);
+    if (tc == 0) rowmax[tr * kRows + i] = m;
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    cm[j] = umax(cm[j], (uint32_t)__shfl_xor((int)cm[j], 16));
-    cm[j] = umax(cm[j], (uint32_t)__shfl_xor((int)cm[j], 32));
+#pragma unroll
+    for (int i = 0; i < kRows; i += 2) cm[j] = max3abs(cm[j], y[i][j], y[i + 1][j]);
+    // (magnitudes compare as their bits)
+    uint32_t m = __float_as_uint(cm[j]);
+    m = umax(m, (uint32_t)__shfl_xor((int)m, 16));
+    cm[j] = __uint_as_float(umax(m, (uint32_t)__shfl_xor((int)m, 32)));
   }
   if (lane < 16) {
 #pragma unroll
@@ -316,31 +377,36 @@ __global__ __launch_bounds__(256) void norm_dual_kernel(NormArgs a, int bt) {
     tile_scale32(rowmax[t], sc, r);
     rrow[t] = r;
     a.s[gcol * a.T + tb * 128 + t] = sc;
-  } else {
+  } else if (t < 256) {
     const int c = t - 128;
+    uint32_t m = __float_as_uint(colred[0][c]);
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) m = umax(m, __float_as_uint(colred[w][c]));
     float sc, r;
-    tile_scale32(umax(umax(colred[0][c], colred[1][c]), umax(colred[2][c], colred[3][c])), sc, r);
+    tile_scale32(__uint_as_float(m), sc, r);
     rcol[c] = r;
     a.sT[tb * a.C + gcol * 128 + c] = sc;
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float r = rrow[tr * 8 + i];
-    const u32x2 o = {cvt4(y[i][0] * r, y[i][1] * r, y[i][2] * r, y[i][3] * r),
-                     cvt4(y[i][4] * r, y[i][5] * r, y[i][6] * r, y[i][7] * r)};
+  for (int i = 0; i < kRows; ++i) {
+    const float r = rrow[tr * kRows + i];
+    const u32x2 o = {codes4(y[i][0] * r, y[i][1] * r, y[i][2] * r, y[i][3] * r),
+                     codes4(y[i][4] * r, y[i][5] * r, y[i][6] * r, y[i][7] * r)};
     __builtin_nontemporal_store(o, reinterpret_cast<u32x2*>(a.q + (tok0 + i) * a.ldq + col0));
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float r = rcol[tc * 8 + j];
-    stage[(tc * 8 + j) * 33 + 2 * tr] = cvt4(y[0][j] * r, y[1][j] * r, y[2][j] * r, y[3][j] * r);
-    stage[(tc * 8 + j) * 33 + 2 * tr + 1] = cvt4(y[4][j] * r, y[5][j] * r, y[6][j] * r, y[7][j] * r);
+#pragma unroll
+    for (int h = 0; h < kRows / 4; ++h)
+      stage[(tc * 8 + j) * 33 + kRows / 4 * tr + h] =
+          codes4(y[4 * h][j] * r, y[4 * h + 1][j] * r, y[4 * h + 2][j] * r, y[4 * h + 3][j] * r);
   }
   __syncthreads();
 #pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    const int cl = (t >> 3) + 32 * it;
+  for (int it = 0; it < 1024 / kDualThreads; ++it) {
+    const int cl = (t >> 3) + kDualThreads / 8 * it;
     const int part = t & 7;
     const uint32_t* sp = stage + cl * 33 + part * 4;
     const u32x4 o = {sp[0], sp[1], sp[2], sp[3]};
@@ -375,7 +441,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, in
   for (int i = 0; i < ITER; ++i) {
     col[i] = 8 * (kTeamThreads * i + tt);
     nv[i] = a.C - col[i] < 0 ? 0 : (a.C - col[i] > 8 ? 8 : a.C - col[i]);
-    load_vec8(a.gamma, a.w_bf16, col[i], nv[i], g[i]);
+    load_vec8(a.gamma, a.w_bf16, aligned16(a.gamma), col[i], nv[i], g[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.f;
   }
@@ -438,7 +504,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, in
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = (__builtin_fmaf(-xh[i][j], s2, d[i][j]) - s1) * rstd;
-      store8<BF16, VEC>(a.dx, row * a.lddx + col[i], ok ? nv[i] : 0, o);
+      store8<BF16, VEC, false>(a.dx, row * a.lddx + col[i], ok ? nv[i] : 0, o);
     }
   }
 
@@ -488,7 +554,13 @@ __global__ __launch_bounds__(256) void norm_bwd_reduce_kernel(const float* __res
   const int which = blockIdx.y;
   float s = 0.f;
   if (c < C)
-    for (int b = ry; b < blocks; b += 16) s += partial[((int64_t)b * 2 + which) * C + c];
+    for (int b0 = ry; b0 < blocks; b0 += 256) {
+      float v[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = b0 + 16 * k < blocks ? partial[((int64_t)(b0 + 16 * k) * 2 + which) * C + c] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) s += v[k];
+    }
   part[ry][cx] = s;
   __syncthreads();
   if (ry == 0 && c < C) {
@@ -526,14 +598,14 @@ hipError_t launch_fwd(NormArgs a, hipStream_t st) {
   };
   if (a.C <= 512) return go(norm_kernel<BF16, VEC, 1, 1, WHAT>, 1);
   if (a.C <= 1024) return go(norm_kernel<BF16, VEC, 1, 2, WHAT>, 1);
-  if (a.C <= 2048) return go(norm_kernel<BF16, VEC, 1, 4, WHAT>, 1);
-  if (a.C <= 4096) return go(norm_kernel<BF16, VEC, 2, 4, WHAT>, 2);
-  if (a.C <= 8192) return go(norm_kernel<BF16, VEC, 4, 4, WHAT>, 4);
+  if (a.C <= 2048) return go(norm_kernel<BF16, VEC, 2, 2, WHAT>, 2);
+  if (a.C <= 4096) return go(norm_kernel<BF16, VEC, 4, 2, WHAT>, 4);
+  if (a.C <= 8192) return go(norm_kernel<BF16, VEC, 8, 2, WHAT>, 8);
   return go(norm_kernel<BF16, VEC, 8, 4, WHAT>, 8);
 }
 
 // waves per row of the backward kernel; its rows per workgroup and step are kBwdWaves / this
-int bwd_wpr(int64_t C) { return C <= 2048 ? 1 : C <= 4096 ? 2 : C <= 8192 ? 4 : 8; }
+int bwd_wpr(int64_t C) { return C <= 1024 ? 1 : C <= 2048 ? 2 : C <= 4096 ? 4 : 8; }
 
 template <bool BF16, bool VEC>
 hipError_t launch_bwd(const NormBwdArgs& a, hipStream_t st) {
@@ -547,9 +619,9 @@ hipError_t launch_bwd(const NormBwdArgs& a, hipStream_t st) {
   hipError_t e;
   if (a.C <= 512) e = go(norm_bwd_kernel<BF16, VEC, 1, 1>);
   else if (a.C <= 1024) e = go(norm_bwd_kernel<BF16, VEC, 1, 2>);
-  else if (a.C <= 2048) e = go(norm_bwd_kernel<BF16, VEC, 1, 4>);
-  else if (a.C <= 4096) e = go(norm_bwd_kernel<BF16, VEC, 2, 4>);
-  else if (a.C <= 8192) e = go(norm_bwd_kernel<BF16, VEC, 4, 4>);
+  else if (a.C <= 2048) e = go(norm_bwd_kernel<BF16, VEC, 2, 2>);
+  else if (a.C <= 4096) e = go(norm_bwd_kernel<BF16, VEC, 4, 2>);
+  else if (a.C <= 8192) e = go(norm_bwd_kernel<BF16, VEC, 8, 2>);
   else e = go(norm_bwd_kernel<BF16, VEC, 8, 4>);
   if (e != hipSuccess || blocks == 1) return e;
   hipLaunchKernelGGL(norm_bwd_reduce_kernel, dim3((unsigned)((a.C + 15) / 16), a.dbeta ? 2 : 1), dim3(256), 0, st,
@@ -574,13 +646,13 @@ hipError_t launch_norm_quant_dual(NormArgs a, hipStream_t st) {
   const hipError_t e = a.x_bf16 ? launch_fwd<true, true, 2>(a, st) : launch_fwd<false, true, 2>(a, st);
   if (e != hipSuccess) return e;
   const int64_t nb = a.T / 128;
-  int bt = 32;   // token blocks per run of workgroups: transposed rows are written in runs (quant.hip, tile_order)
-  while (nb % bt) bt >>= 1;
+  int bt = 5;   // up to 32 token blocks per run of workgroups: transposed rows are written in 4 KB runs
+  while (nb & ((int64_t(1) << bt) - 1)) --bt;
   const dim3 grid((unsigned)(nb * (a.C / 128)));
   if (a.x_bf16)
-    hipLaunchKernelGGL(norm_dual_kernel<true>, grid, dim3(256), 0, st, a, bt);
+    hipLaunchKernelGGL(norm_dual_kernel<true>, grid, dim3(kDualThreads), 0, st, a, bt);
   else
-    hipLaunchKernelGGL(norm_dual_kernel<false>, grid, dim3(256), 0, st, a, bt);
+    hipLaunchKernelGGL(norm_dual_kernel<false>, grid, dim3(kDualThreads), 0, st, a, bt);
   return hipGetLastError();
 }
 

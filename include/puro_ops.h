@@ -50,7 +50,8 @@ int puro_layer_norm(int kind, int x_dtype, const void* x, int64_t T, int64_t C, 
  * Norm of each row, written as the 1x128 codes and scales an FP8 product reads (layouts of
  * puro_fp8_quant_act_1x128): q uint8 [T, C] (row stride ldq), s fp32 [C/128][T].  The group maximum,
  * scale and codes come from the fp32 norm (one rounding, to E4M3; the numerics of puro_fp8.h with
- * the fp32 value in place of the bf16 one), so y itself is never written.  Any T >= 0; C % 128 == 0.
+ * the fp32 value in place of the bf16 one), so y itself is never written.  A NaN has a NaN code and does not
+ * enter its group's scale.  Any T >= 0; C % 128 == 0.
  * x, q and s 16-byte aligned, rows a multiple of 16 bytes apart, as in puro_fp8.h; weight and bias
  * 16-byte aligned.  mean and rstd as in puro_layer_norm.
  */
@@ -62,8 +63,7 @@ int puro_layer_norm_quant(int kind, int x_dtype, const void* x, int64_t T, int64
  * As puro_layer_norm_quant, with the transposed 128x1 codes of the same fp32 norm as well (layouts of
  * puro_fp8_quant_act_dual): qT uint8 [C, T] (row stride ldqT), sT fp32 [T/128][C].  The training form:
  * q feeds FWD, qT feeds WGRAD.  T % 128 == 0, C % 128 == 0.  rstd is required, and so is mean for
- * PURO_NORM_LAYER: the second launch reads them.  q and s equal puro_layer_norm_quant's up to the
- * last bit of the fp32 norm (the multiplications are the same; the compiler may fuse them differently).
+ * PURO_NORM_LAYER: the second launch reads them.  q and s are puro_layer_norm_quant's, bit for bit.
  */
 int puro_layer_norm_quant_dual(int kind, int x_dtype, const void* x, int64_t T, int64_t C, int64_t ldx, int w_dtype,
                                const void* weight, const void* bias, float eps, uint8_t* q, int64_t ldq, float* s,

@@ -144,6 +144,13 @@ def test_norm_empty(P):
     assert y.shape == (3, 0)
 
 
+def folded(by, x, w, rr, rm):
+    """The quantized forms compute (x r - mu r) g + b in two FMAs: besides the bound of y, one rounding of mu r and
+    one of the difference, whose terms are |x| r and |mu| r."""
+    r, m = rr[:, None], rm[:, None]
+    return by + 2 * U * w.double().abs() * r * (m.abs() + (x.double() - m).abs())
+
+
 def codes_near(P, q, s, y, by, what):
     """Codes q [R, K] and scales s [K/128, R] against the fp64 norm y [R, K] with error bound by.  The scale is the
     group's maximum / 448 (three roundings); a code times its scale is within half an E4M3 step of y (2^-4 of the value,
@@ -175,8 +182,8 @@ def test_norm_quant_rows(P, T, C):
                                        mean=mean, rstd=rstd)
         y, m, r = P.puro_layer_norm(x, w, b, kind=kind)
         assert t.equal(r, rstd) and (kind == 1 or t.equal(m, mean))
-        ry, _, _, by, _, _ = reference(x, w, b, 1e-5, kind)
-        codes_near(P, q, s, ry, by, "1x128")
+        ry, rm, rr, by, _, _ = reference(x, w, b, 1e-5, kind)
+        codes_near(P, q, s, ry, folded(by, x, w, rr, rm), "1x128")
 
 
 @pytest.mark.parametrize("T,C", [(128, 128), (256, 384), (384, 2048), (128, 4224), (4096, 256), (128, 16384)])
@@ -190,13 +197,14 @@ def test_norm_quant_dual(P, T, C):
         y, m, r = P.puro_layer_norm(x, w, b, kind=kind)
         assert t.equal(q, q1) and t.equal(s, s1), "the two forms' row codes differ"
         assert t.equal(r, rstd) and (kind == 1 or t.equal(m, mean))
-        ry, _, _, by, _, _ = reference(x, w, b, 1e-5, kind)
+        ry, rm, rr, by, _, _ = reference(x, w, b, 1e-5, kind)
+        by = folded(by, x, w, rr, rm)
         codes_near(P, qT, sT, ry.t().contiguous(), by.t().contiguous(), "128x1")
 
 
 def test_norm_quant_special_groups(P):
-    """A zero group gets the floor's scale and zero codes; a NaN row gives NaN scales and codes in that row alone; the
-    scale of an RMS row of one repeated value is that value's."""
+    """A zero group gets the floor's scale and zero codes; a row with a NaN gives NaN codes in that row alone, whose
+    scales and those of the other rows it does not touch."""
     t = torch()
     x = t.randn((128, 256), device="cuda").bfloat16()
     w = t.ones(256, device="cuda")
@@ -206,9 +214,17 @@ def test_norm_quant_special_groups(P):
     assert (qT[128:] & 0x7F == 0).all()
     x[3, 7] = float("nan")
     q2, s2 = P.puro_layer_norm_quant(x, w, kind=1)
-    assert s2[0, 3].isnan() and (q2[3] & 0x7F == 0x7F).all()
+    assert (q2[3] & 0x7F == 0x7F).all()
     keep = [i for i in range(128) if i != 3]
     assert t.equal(q2[keep], q[keep]) and t.equal(s2[:, keep], s[:, keep])
+    q3, s3, qT3, sT3, _, _ = P.puro_layer_norm_quant_dual(x, w, kind=1)
+    assert t.equal(q3, q2) and t.equal(s3, s2) and (qT3[:, 3] & 0x7F == 0x7F).all() and sT3.isfinite().all()
+    x[3, 7] = x[3, 8]
+    x[:, 9] = 0
+    rest = P.puro_layer_norm_quant_dual(x, w, kind=1)
+    x[3, 9] = float("nan")
+    bad = P.puro_layer_norm_quant_dual(x, w, kind=1)
+    assert (bad[2][:, keep] == rest[2][:, keep]).float().mean() > 0.9    # a column's maximum may have been row 3's
 
 
 def ref_backward(dy, x, w, mean, rstd, kind):
