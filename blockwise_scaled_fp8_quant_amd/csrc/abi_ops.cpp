@@ -14,6 +14,7 @@ namespace {
 
 constexpr int64_t kGroup = 128;
 constexpr int64_t kIntMax = 0x7FFFFFFF;
+constexpr int64_t kMaxGemmLd = int64_t(1) << 29;   // as puro_fp8_gemm: leading rows may run its kernels
 
 inline bool aligned(const void* p, int64_t n) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0; }
 inline bool dtype_ok(int d) { return d == PURO_OUT_BF16 || d == PURO_OUT_FP32; }
@@ -269,11 +270,12 @@ int puro_gemm_rows(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t ld
     if (lda < K || ldb < K || lda % 16 || ldb % 16) return PURO_ERR_LD;
   }
   if (M > kIntMax || N > kIntMax || K > kIntMax) return PURO_ERR_UNSUPPORTED;
-  const size_t need = puro_gemm_rows_workspace_size(M, N, K);
+  if (K > 0 && (lda > kMaxGemmLd || ldb > kMaxGemmLd)) return PURO_ERR_UNSUPPORTED;
+  const size_t need = out_dtype == PURO_OUT_BF16 ? puro_gemm_rows_workspace_size(M, N, K) : 0;
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PURO_ERR_WORKSPACE;
   if (need > 0 && !aligned(workspace, 16)) return PURO_ERR_ALIGN;
   return from_hip(puro::launch_gemm_rows(M, N, K, A, lda, sA, B, ldb, sB, C, ldc, out_dtype == PURO_OUT_BF16, workspace,
-                                         st));
+                                         workspace_bytes, st));
 }
 
 }  // extern "C"

@@ -625,7 +625,7 @@ size_t gemm_workspace_bytes(int, int64_t M, int64_t N, int64_t K) {
 hipError_t launch_gemm(int mode, int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda,
                        const float* sA, const uint8_t* B, int64_t ldb, const float* sB, void* C,
                        int64_t ldc, bool out_bf16, bool accumulate, uint8_t* q, int64_t ldq, float* qs,
-                       void* workspace, size_t workspace_bytes, hipStream_t st) {
+                       void* workspace, size_t workspace_bytes, hipStream_t st, int64_t ldsa) {
   if (accumulate && out_bf16) return hipErrorInvalidValue;
   if (q != nullptr && !out_bf16) return hipErrorInvalidValue;
   if (K == 0) {
@@ -655,7 +655,7 @@ hipError_t launch_gemm(int mode, int64_t M, int64_t N, int64_t K, const uint8_t*
     const GemmPart& pt = parts[i];
     // sA (and the MX E8M0 tiles, 4 bytes per row) and the output scales of row r start r elements in
     const hipError_t e =
-        launch_rows(mode, pt.rows, N, K, pt.splits, A + pt.row0 * lda, lda, sA + pt.row0, M, B, ldb, sB,
+        launch_rows(mode, pt.rows, N, K, pt.splits, A + pt.row0 * lda, lda, sA + pt.row0, ldsa ? ldsa : M, B, ldb, sB,
                     static_cast<uint8_t*>(C) + pt.row0 * ldc * es, ldc, out_bf16, accumulate,
                     q ? q + pt.row0 * ldq : nullptr, ldq, q ? qs + pt.row0 : nullptr, M, workspace,
                     workspace_bytes, st);

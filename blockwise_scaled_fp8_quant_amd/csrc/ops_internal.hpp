@@ -79,9 +79,10 @@ hipError_t launch_grad_scale(const GradJob* jobs, int n_jobs, const double* part
                              const float* norm_in, float* norm_out, float max_norm, hipStream_t st);
 
 // ---- few-row product (gemm_rows.hip) ----------------------------------------------------------------
+// (of a bf16 output; an fp32 one needs none)
 size_t gemm_rows_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_rows(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda, const float* sA,
                             const uint8_t* B, int64_t ldb, const float* sB, void* C, int64_t ldc, bool out_bf16,
-                            void* workspace, hipStream_t st);
+                            void* workspace, size_t workspace_bytes, hipStream_t st);
 
 }  // namespace puro

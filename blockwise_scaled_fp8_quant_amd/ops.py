@@ -352,7 +352,8 @@ def puro_gemm_rows(A, sA, B, sB, C=None, out_dtype: int = OUT_BF16, workspace=No
     if out_dtype not in (OUT_BF16, OUT_FP32):
         raise ValueError(f"out_dtype {out_dtype}: expected OUT_BF16 or OUT_FP32")
     C, ldc = _out_rows(C, "C", torch.bfloat16 if out_dtype == OUT_BF16 else _f32t, (M, N), dev)
-    workspace, pws, wbytes = _workspace(workspace, lib.puro_gemm_rows_workspace_size(M, N, K), dev)
+    need = lib.puro_gemm_rows_workspace_size(M, N, K) if out_dtype == OUT_BF16 else 0
+    workspace, pws, wbytes = _workspace(workspace, need, dev)
     _check(lib.puro_gemm_rows(M, N, K, A.data_ptr(), lda, psA, B.data_ptr(), ldb, psB, C.data_ptr(), ldc, out_dtype, pws,
                               wbytes, _raw_stream(dev)), "puro_gemm_rows")
     return C

@@ -63,6 +63,21 @@ def test_every_row_count(P, N, K):
     say(f"    fp32 relative error {e32:.2e}")
 
 
+@pytest.mark.parametrize("M,N,K", [(1061, 4096, 2048), (1024, 512, 16384), (1026, 512, 16512)])
+def test_long_products(P, M, N, K):
+    """Leading rows of a long bf16 product are the blockwise GEMM's, bit for bit, with a contraction split and
+    without; the rest, and an fp32 output throughout, keep the bound above."""
+    t = torch()
+    A, sA, B, sB = operands(M, N, K, 2)
+    lead = M - M % 128
+    C = P.puro_gemm_rows(A, sA, B, sB)
+    want = P.puro_fp8_gemm(P.FWD, A[:lead], sA[:, :lead].contiguous(), B, sB)
+    assert t.equal(C[:lead], want)
+    if lead < M:
+        check(P, A[lead:], sA[:, lead:].contiguous(), B, sB, C[lead:], t.bfloat16, "rest")
+    check(P, A, sA, B, sB, P.puro_gemm_rows(A, sA, B, sB, out_dtype=P.OUT_FP32), t.float32, "fp32")
+
+
 def test_strides_and_gaps(P):
     t = torch()
     for M, N, K in ((5, 256, 256), (40, 384, 512), (130, 128, 256)):
