@@ -21,9 +21,11 @@ namespace {
 
 constexpr int kMaxJobs = 112;              // 112 * 32 + 128 bytes: inside the 4 KB of kernel arguments
 constexpr int kThreads = 256;
-constexpr int kVecs = 8;                   // 16-byte loads a thread has in flight
-constexpr int kChunkBytes = kThreads * kVecs * 16;   // 32 KB of a tensor per step of a workgroup
-constexpr int kMaxBlocks = 2048;           // workgroups of a launch: 8 per CU
+// 16-byte loads a thread has in flight, and workgroups of a launch (8 per CU).  Measured on 1.6 GB of fp32
+// gradients, norm + scaling: 252 + 566 us.  With 8 loads the scaling takes 627 us, with 1024 workgroups 577, with
+// 512 742; past-the-cache loads take 23 us off the norm and put 18 to 30 on the scaling.
+constexpr int kVecs = 4;
+constexpr int kMaxBlocks = 2048;
 
 struct JobDesc {
   const uint8_t* src;

@@ -73,8 +73,8 @@ struct Operand {
       : v{decode8(f.w[0].x, f.w[0].y), decode8(f.w[0].z, f.w[0].w), decode8(f.w[1].x, f.w[1].y), decode8(f.w[1].z, f.w[1].w)} {}
 };
 
-// MT x NT tiles of 16 x 16, the contraction over WK waves, DEPTH slices of a wave in flight.
-template <int MT, int NT, int WK, int DEPTH, bool OUT_BF16>
+// MT x NT tiles of 16 x 16, the contraction over WK waves.
+template <int MT, int NT, int WK, bool OUT_BF16>
 __global__ __launch_bounds__(64 * WK) void gemm_rows_kernel(RowsArgs p) {
   constexpr int kTiles = MT * NT;
   constexpr int kStage = (MT + NT) * 2048;
@@ -122,66 +122,66 @@ __global__ __launch_bounds__(64 * WK) void gemm_rows_kernel(RowsArgs p) {
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   const int per = (nk + WK - 1) / WK, kbeg = wave * per, kend = kbeg + per < nk ? kbeg + per : nk;
-  for (int kb0 = kbeg; kb0 < kend; kb0 += DEPTH) {
-    u32x4 bl[DEPTH][NT][2], al[DEPTH][MT][2];
-    float sa[DEPTH][MT];
+  // Up to 32 rows and 3 strips the next slice is loaded as soon as this one is in LDS (1 x 6144 deep x 2048: 6.2 us, 7.4
+  // without).  Larger tiles lack the registers: 64 x 2048 deep x 4096 takes 9.8 us so and 5.7 as it is, one row with 4 strips
+  // (151936 columns) 69.7 and 59.1.
+  constexpr bool kAhead = MT <= 2 && NT <= 3;
+  u32x4 bl[NT][2], al[MT][2];
+  float sa[MT];
+  auto fetch = [&](int kb) {
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-      const int kb = kb0 + d;
-      if (kb < kend) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          bl[d][j][0] = *reinterpret_cast<const u32x4*>(bp[j] + (int64_t)kb * 128);
-          bl[d][j][1] = *reinterpret_cast<const u32x4*>(bp[j] + 8 * p.ldb + (int64_t)kb * 128);
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) al[d][i][h] = *reinterpret_cast<const u32x4*>(ap[i][h] + (int64_t)kb * 128);
-          sa[d][i] = p.sA[(int64_t)kb * p.lds + mrow[i]];
-        }
-      }
+    for (int j = 0; j < NT; ++j) {
+      bl[j][0] = *reinterpret_cast<const u32x4*>(bp[j] + (int64_t)kb * 128);
+      bl[j][1] = *reinterpret_cast<const u32x4*>(bp[j] + 8 * p.ldb + (int64_t)kb * 128);
     }
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-      if (kb0 + d < kend) {
+    for (int i = 0; i < MT; ++i) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          *reinterpret_cast<u32x4*>(wr0 + j * 2048) = bl[d][j][0];
-          *reinterpret_cast<u32x4*>(wr1 + j * 2048) = bl[d][j][1];
-        }
+      for (int h = 0; h < 2; ++h) al[i][h] = *reinterpret_cast<const u32x4*>(ap[i][h] + (int64_t)kb * 128);
+      sa[i] = p.sA[(int64_t)kb * p.lds + mrow[i]];
+    }
+  };
+  if (kAhead && kbeg < kend) fetch(kbeg);
+  for (int kb = kbeg; kb < kend; ++kb) {
+    if (!kAhead) fetch(kb);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          *reinterpret_cast<u32x4*>(wr0 + (NT + i) * 2048) = al[d][i][0];
-          *reinterpret_cast<u32x4*>(wr1 + (NT + i) * 2048) = al[d][i][1];
-        }
-        wave_order();   // the LDS piece is the wave's own: its instructions reach it in order
-        auto fragment = [&](int f) {
-          return Operand(Frag{*reinterpret_cast<const u32x4*>(rd0 + f * 2048), *reinterpret_cast<const u32x4*>(rd1 + f * 2048)});
-        };
-        bf16x8_t bv[NT][4];
+    for (int j = 0; j < NT; ++j) {
+      *reinterpret_cast<u32x4*>(wr0 + j * 2048) = bl[j][0];
+      *reinterpret_cast<u32x4*>(wr1 + j * 2048) = bl[j][1];
+    }
+    float sc[MT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const Operand b = fragment(j);
+    for (int i = 0; i < MT; ++i) {
+      *reinterpret_cast<u32x4*>(wr0 + (NT + i) * 2048) = al[i][0];
+      *reinterpret_cast<u32x4*>(wr1 + (NT + i) * 2048) = al[i][1];
+      sc[i] = sa[i];
+    }
+    if (kAhead && kb + 1 < kend) fetch(kb + 1);
+    wave_order();   // the LDS piece is the wave's own: its instructions reach it in order
+    auto fragment = [&](int f) {
+      return Operand(Frag{*reinterpret_cast<const u32x4*>(rd0 + f * 2048), *reinterpret_cast<const u32x4*>(rd1 + f * 2048)});
+    };
+    bf16x8_t bv[NT][4];
 #pragma unroll
-          for (int h = 0; h < 4; ++h) bv[j][h] = b.v[h];
-        }
+    for (int j = 0; j < NT; ++j) {
+      const Operand b = fragment(j);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const Operand a = fragment(NT + i);
+      for (int h = 0; h < 4; ++h) bv[j][h] = b.v[h];
+    }
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < MT; ++i) {
+      const Operand a = fragment(NT + i);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[j][h], a.v[h], v, 0, 0, 0);
-            const float s = sa[d][i] * sb[j][kb0 + d];
+      for (int j = 0; j < NT; ++j) {
+        f32x4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(v[r], s, acc[i][j][r]);
-          }
-        }
-        wave_order();
+        for (int h = 0; h < 4; ++h) v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[j][h], a.v[h], v, 0, 0, 0);
+        const float s = sc[i] * sb[j][kb];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(v[r], s, acc[i][j][r]);
       }
     }
+    wave_order();
   }
   __syncthreads();
 
@@ -207,28 +207,28 @@ __global__ __launch_bounds__(64 * WK) void gemm_rows_kernel(RowsArgs p) {
   }
 }
 
-template <int MT, int NT, int WK, int DEPTH>
+template <int MT, int NT, int WK>
 hipError_t go(const RowsArgs& a, bool out_bf16, hipStream_t st) {
   const dim3 grid((unsigned)((a.N + 16 * NT - 1) / (16 * NT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
   if (grid.y > 65535u) return hipErrorInvalidConfiguration;   // over 4 million fp32 rows
   if (out_bf16)
-    hipLaunchKernelGGL((gemm_rows_kernel<MT, NT, WK, DEPTH, true>), grid, dim3(64 * WK), 0, st, a);
+    hipLaunchKernelGGL((gemm_rows_kernel<MT, NT, WK, true>), grid, dim3(64 * WK), 0, st, a);
   else
-    hipLaunchKernelGGL((gemm_rows_kernel<MT, NT, WK, DEPTH, false>), grid, dim3(64 * WK), 0, st, a);
+    hipLaunchKernelGGL((gemm_rows_kernel<MT, NT, WK, false>), grid, dim3(64 * WK), 0, st, a);
   return hipGetLastError();
 }
 
 // Strips per workgroup: the fewest that leave at most one workgroup per CU (256).  Fewer would give some CUs two and others one
 // (N = 12288, M <= 16: 7.0 us with 3 strips, 8.6 with 1), more would leave CUs idle (N = 4096: 4.1 us with 1,
-// 4.5 with 2).  A lone strip gets 16 waves (K = 6144: 6.9 us, 7.5 with 8).
-template <int MT, int DEPTH1>
+// 4.5 with 2).  A lone strip gets 16 waves (K = 6144: 6.5 us, 7.2 with 8).
+template <int MT>
 hipError_t by_strips(const RowsArgs& a, bool out_bf16, hipStream_t st) {
   const int64_t strips = a.N / 16, row_blocks = (a.M + 16 * MT - 1) / (16 * MT);
   auto fits = [&](int64_t nt) { return (strips + nt - 1) / nt * row_blocks <= 256; };
-  if (fits(1)) return go<MT, 1, 16, DEPTH1>(a, out_bf16, st);
-  if (fits(2)) return go<MT, 2, 8, 1>(a, out_bf16, st);
-  if (fits(3)) return go<MT, 3, 8, 1>(a, out_bf16, st);
-  return go<MT, 4, 8, 1>(a, out_bf16, st);
+  if (fits(1)) return go<MT, 1, 16>(a, out_bf16, st);
+  if (fits(2)) return go<MT, 2, 8>(a, out_bf16, st);
+  if (fits(3)) return go<MT, 3, 8>(a, out_bf16, st);
+  return go<MT, 4, 8>(a, out_bf16, st);
 }
 
 // Leading rows (a multiple of 128) that go through the 256 x 256 tiles of the blockwise GEMM: all there are, where their
@@ -258,9 +258,9 @@ hipError_t launch_gemm_rows(int64_t M, int64_t N, int64_t K, const uint8_t* A, i
   const int64_t rows = M - lead;
   const RowsArgs a = {(int)rows, (int)N, (int)K, A + lead * lda, lda, sA + lead, M, B, ldb, sB,
                       static_cast<uint8_t*>(C) + lead * ldc * (out_bf16 ? 2 : 4), ldc};
-  if (rows <= 16) return by_strips<1, 2>(a, out_bf16, st);
-  if (rows <= 32) return by_strips<2, 2>(a, out_bf16, st);
-  return by_strips<4, 1>(a, out_bf16, st);
+  if (rows <= 16) return by_strips<1>(a, out_bf16, st);
+  if (rows <= 32) return by_strips<2>(a, out_bf16, st);
+  return by_strips<4>(a, out_bf16, st);
 }
 
 }  // namespace puro

@@ -156,9 +156,9 @@ def test_grad_workspace_size():
     size = P.lib.puro_grad_norm_workspace_size
     assert size(jobs(), 0) == 0 and size(jobs((A16, None, 0, FP32)), 1) == 0
     assert size(jobs((A16, None, 1, FP32)), 1) == 8
-    # 8192 fp32 elements make one step of a workgroup; one more needs a second, and so does a start off 16 bytes
-    assert size(jobs((A16, None, 8192, FP32)), 1) == 8 and size(jobs((A16, None, 8193, FP32)), 1) == 16
-    assert size(jobs((A16 + 4, None, 8192, FP32)), 1) == 16
+    # 4096 fp32 elements make one step of a workgroup; one more needs a second, and so does a start off 16 bytes
+    assert size(jobs((A16, None, 4096, FP32)), 1) == 8 and size(jobs((A16, None, 4097, FP32)), 1) == 16
+    assert size(jobs((A16 + 4, None, 4096, FP32)), 1) == 16
     assert size(jobs(*[(A16, None, 1, BF16)] * 300), 300) == 300 * 8
     assert size(jobs((A16, None, 1, 9)), 1) == 0
 
