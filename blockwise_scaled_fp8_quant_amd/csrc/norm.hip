@@ -277,7 +277,9 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs
       }
       sq += nv[i] > 0 ? part : 0.f;
     }
-    const float rstd = 1.0f / __builtin_sqrtf(team_sum<WPR, kWaves>(sq, red, 1, wave) * inv_c + a.eps);
+    // (an RMS norm has this sum alone, so it takes the LDS rows in turn from row to row)
+    const float rstd =
+        1.0f / __builtin_sqrtf(team_sum<WPR, kWaves>(sq, red, a.layer ? 1 : (k & 1), wave) * inv_c + a.eps);
     if (ok && tt == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;

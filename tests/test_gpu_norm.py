@@ -98,6 +98,29 @@ def test_norm_forward(P, T, C):
             assert mean is None
 
 
+@pytest.mark.parametrize("T,C", [(8200, 2048), (4099, 4096), (2053, 8192), (2051, 16384), (16390, 640)])
+def test_norm_many_rows(P, T, C):
+    """Long inputs, where a team of waves takes several rows in turn: every row as by itself."""
+    t = torch()
+    for kind in (0, 1):
+        say(f"[norm, many rows] {T}x{C} kind {kind}")
+        x, w, b = inputs(T, C, t.bfloat16, t.bfloat16, kind, T)
+        y, mean, rstd = P.puro_layer_norm(x, w, b, kind=kind)
+        q, s = P.puro_layer_norm_quant(x, w, b, kind=kind)
+        for lo in range(0, T, 500):                 # 500 rows at a time: one row per team
+            part = slice(lo, min(lo + 500, T))
+            y1, m1, r1 = P.puro_layer_norm(x[part], w, b, kind=kind)
+            q1, s1 = P.puro_layer_norm_quant(x[part], w, b, kind=kind)
+            assert t.equal(y[part], y1) and t.equal(rstd[part], r1) and (kind == 1 or t.equal(mean[part], m1))
+            assert t.equal(q[part], q1) and t.equal(s[:, part], s1)
+        ry, rm, rr, by, _, br = reference(x[-40:], w, b, 1e-5, kind)
+        near(y[-40:], ry, by + half_step(ry, t.bfloat16), "y")
+        near(rstd[-40:], rr, rr * br, "rstd")
+        T128 = T // 128 * 128
+        d = P.puro_layer_norm_quant_dual(x[:T128], w, b, kind=kind)
+        assert t.equal(d[0], q[:T128]) and t.equal(d[1], s[:, :T128]) and t.equal(d[5], rstd[:T128])
+
+
 def test_norm_leaves_gaps_alone_and_runs_in_place(P):
     t = torch()
     x, w, b = inputs(5, 100, t.bfloat16, t.float32, 0, 3)
@@ -245,7 +268,7 @@ def ref_backward(dy, x, w, mean, rstd, kind):
 
 
 @pytest.mark.parametrize("T,C", [(1, 1), (1, 8), (2, 7), (17, 100), (16, 512), (65, 512), (300, 1000), (1027, 1000), (40, 2048),
-                                 (513, 2048), (5, 4096), (33, 4100), (9, 8192), (1, 16384), (19, 16376), (4500, 256)])
+                                 (513, 2048), (5, 4096), (33, 4100), (9, 8192), (1, 16384), (19, 16376), (4500, 256), (6001, 2048), (2100, 4096), (1300, 8192)])
 def test_norm_backward(P, T, C):
     t = torch()
     for (dtype, wdtype), kind, pad in itertools.product(((t.bfloat16, t.bfloat16), (t.float32, t.float32), (t.bfloat16, t.float32)),
