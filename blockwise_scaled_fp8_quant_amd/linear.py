@@ -39,9 +39,10 @@ __all__ = ["Fp8LinearFunction", "Fp8Linear", "fp8_linear"]
 
 
 def _rows(t: torch.Tensor, width: int) -> torch.Tensor:
-    """View as [rows, width] with unit column stride (copies only a non-viewable layout)."""
+    """View as [rows, width] with unit column stride and rows apart from each other (copies only a layout
+    that has no such view, such as a gradient broadcast over the rows)."""
     t2 = t.reshape(-1, width)
-    return t2 if t2.stride(1) == 1 else t2.contiguous()
+    return t2 if t2.stride(1) == 1 and (t2.stride(0) >= width or t2.shape[0] <= 1) else t2.contiguous()
 
 
 class Fp8LinearFunction(torch.autograd.Function):

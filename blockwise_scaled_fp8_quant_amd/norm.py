@@ -20,6 +20,7 @@ Fp8Linear.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (DGRAD, FWD, LAYER_NORM, OUT_BF16, OUT_FP32, RMS_NORM, WGRAD, puro_fp8_gemm, puro_fp8_gemm_accumulate,
                puro_fp8_quant_act_dual, puro_fp8_quant_w_128x128, puro_gemm_rows, puro_layer_norm,
@@ -29,9 +30,9 @@ from .linear import Fp8Linear, _rows
 __all__ = ["Norm", "NormFunction", "Fp8NormLinear", "Fp8NormLinearFunction", "layer_norm", "rms_norm"]
 
 
-def _norm_grads(ctx, dn, x2, weight, bias, mean, rstd, need_w, need_b):
-    """dx and the weight's and bias's gradients of the norm; those with a main_grad are added into it and
-    returned as None."""
+def _norm_grads(kind, dn, x2, gamma, mean, rstd, weight, bias, need_w, need_b):
+    """dx and the weight's and bias's gradients of the norm (gamma: the weight as the forward pass saw it); those with
+    a main_grad are added into it and returned as None."""
     main_w = getattr(weight, "main_grad", None) if need_w else None
     main_b = getattr(bias, "main_grad", None) if need_b else None
     if need_w and need_b and (main_w is None) != (main_b is None):
@@ -41,7 +42,7 @@ def _norm_grads(ctx, dn, x2, weight, bias, mean, rstd, need_w, need_b):
         # the kernel adds into both; a parameter that needs no gradient gets a scratch tensor
         if main_w is None:
             main_w = torch.zeros(weight.shape, dtype=torch.float32, device=weight.device)
-    dx, dw, db = puro_layer_norm_backward(dn, x2, weight, mean, rstd, kind=ctx.kind, dweight=main_w, dbias=main_b,
+    dx, dw, db = puro_layer_norm_backward(dn, x2, gamma, mean, rstd, kind=kind, dweight=main_w, dbias=main_b,
                                           with_bias=need_b, accumulate=main)
     if main:
         return dx, None, None
@@ -53,14 +54,15 @@ class NormFunction(torch.autograd.Function):
     def forward(ctx, x, weight, bias, eps, kind):
         x2 = _rows(x, x.shape[-1])
         y, mean, rstd = puro_layer_norm(x2, weight, bias, eps=eps, kind=kind)
-        ctx.save_for_backward(x2, mean, rstd)
+        ctx.save_for_backward(x2, weight, mean, rstd)
         ctx.weight, ctx.bias, ctx.kind, ctx.x_shape = weight, bias, kind, x.shape
         return y.view(x.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
-        x2, mean, rstd = ctx.saved_tensors
-        dx, dw, db = _norm_grads(ctx, _rows(dy, x2.shape[1]), x2, ctx.weight, ctx.bias, mean, rstd,
+        x2, gamma, mean, rstd = ctx.saved_tensors
+        dx, dw, db = _norm_grads(ctx.kind, _rows(dy, x2.shape[1]), x2, gamma, mean, rstd, ctx.weight, ctx.bias,
                                  ctx.needs_input_grad[1], ctx.bias is not None and ctx.needs_input_grad[2])
         return dx.view(ctx.x_shape), dw, db, None, None
 
@@ -104,13 +106,14 @@ class Fp8NormLinearFunction(torch.autograd.Function):
         xq, xs, xqT, xsT, mean, rstd = puro_layer_norm_quant_dual(x2, norm_weight, norm_bias, eps=eps, kind=kind)
         wq, ws, wqT, wsT = puro_fp8_quant_w_128x128(_rows(weight, din))
         y = puro_fp8_gemm(FWD, xq, xs, wq, ws, out_dtype=OUT_BF16)
-        ctx.save_for_backward(x2, mean, rstd, xqT, xsT, wqT, wsT)
+        ctx.save_for_backward(x2, norm_weight, mean, rstd, xqT, xsT, wqT, wsT)
         ctx.params, ctx.kind, ctx.x_shape = (norm_weight, norm_bias, weight), kind, x.shape
         return y.view(*x.shape[:-1], dout)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
-        x2, mean, rstd, xqT, xsT, wqT, wsT = ctx.saved_tensors
+        x2, gamma, mean, rstd, xqT, xsT, wqT, wsT = ctx.saved_tensors
         norm_weight, norm_bias, weight = ctx.params
         if dy.dtype != torch.bfloat16:
             raise TypeError("Fp8NormLinear expects a bf16 output gradient")
@@ -119,7 +122,7 @@ class Fp8NormLinearFunction(torch.autograd.Function):
         dx = dnw = dnb = dw = None
         if any(need[:3]):
             dn = puro_fp8_gemm(DGRAD, gq, gs, wqT, wsT, out_dtype=OUT_BF16 if x2.dtype == torch.bfloat16 else OUT_FP32)
-            dx, dnw, dnb = _norm_grads(ctx, dn, x2, norm_weight, norm_bias, mean, rstd, need[1],
+            dx, dnw, dnb = _norm_grads(ctx.kind, dn, x2, gamma, mean, rstd, norm_weight, norm_bias, need[1],
                                        norm_bias is not None and need[2])
             dx = dx.view(ctx.x_shape)
         if need[3]:

@@ -127,6 +127,48 @@ def test_norm_module_gradients(P):
     assert t.equal(rms_norm(x, w), P.puro_layer_norm(x, w, eps=1e-6, kind=P.RMS_NORM)[0])
 
 
+def test_broadcast_gradients_and_changed_weights(P):
+    """A gradient broadcast over rows (of a sum over them) is taken; a weight changed between the passes is refused;
+    so is a second derivative."""
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.norm import Norm
+    n = Norm(256, 0, device="cuda")
+    x = t.randn((128, 256), device="cuda").bfloat16().requires_grad_(True)
+    g = t.randn(256, device="cuda").bfloat16()
+    n(x).sum(0).backward(g)
+    dx, n.weight.grad, n.bias.grad, x.grad = x.grad, None, None, None
+    n(x).backward(g.expand(128, 256).contiguous())
+    assert t.equal(dx, x.grad)
+    m = layer(P, 1)
+    x = t.randn((128, 256), device="cuda").bfloat16().requires_grad_(True)
+    m(x).sum(0).backward(t.ones(384, device="cuda").bfloat16())
+    assert x.grad.isfinite().all()
+    for mod, param in ((n, n.weight), (m, m.norm.weight)):
+        y = mod(x)
+        with t.no_grad():
+            param.mul_(2)
+        with pytest.raises(RuntimeError):
+            y.backward(t.ones_like(y))
+    y = n(x)
+    (first,) = t.autograd.grad(y.float().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        first.float().sum().backward()
+
+
+def test_frozen_parameters_get_nothing(P):
+    t = torch()
+    m = layer(P, 0)
+    m.enable_main_grad()
+    m.norm.weight.requires_grad_(False)
+    x = t.randn((128, 256), device="cuda").bfloat16().requires_grad_(True)
+    m(x).backward(t.ones((128, 384), device="cuda").bfloat16())
+    assert (m.norm.weight.main_grad == 0).all() and (m.norm.bias.main_grad != 0).any() and x.grad is not None
+    m.norm.bias.requires_grad_(False)
+    kept = m.norm.bias.main_grad.clone()
+    m(x).backward(t.ones((128, 384), device="cuda").bfloat16())
+    assert t.equal(m.norm.bias.main_grad, kept)
+
+
 def test_step_with_clipping(P):
     """Forward, backward and clipping of two stacked layers: afterwards the global norm is the bound."""
     t = torch()

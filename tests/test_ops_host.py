@@ -177,7 +177,7 @@ def test_rows_refusals():
         assert rows(**{a: MIS}) == ALIGN, a
     assert rows(sA=A16 + 2) == ALIGN and rows(sB=A16 + 1) == ALIGN
     assert rows(lda=128) == LD and rows(ldb=264) == LD and rows(ldc=128) == LD and rows(ldc=260) == LD
-    assert rows(M=1 << 32) == UNSUP and rows(lda=(1 << 29) + 16) == UNSUP and rows(ldb=(1 << 29) + 16) == UNSUP
+    assert rows(M=1 << 32) == UNSUP and rows(N=1 << 30, ldc=1 << 30) == UNSUP and rows(lda=(1 << 29) + 16) == UNSUP and rows(ldb=(1 << 29) + 16) == UNSUP
     # a long product whose leading rows the blockwise GEMM splits over the contraction wants its workspace for bf16
     big = dict(M=1030, N=512, K=1 << 14, lda=1 << 14, ldb=1 << 14, ldc=512)
     need = P.puro_gemm_rows_workspace_size(1030, 512, 1 << 14)
