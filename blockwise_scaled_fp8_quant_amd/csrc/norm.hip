@@ -25,93 +25,133 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // ---- eight consecutive columns of a row -------------------------------------------------------------
-// VEC: 16-byte aligned, either all eight exist or none.  Otherwise element by element, nv of them.
+// VEC: 16-byte aligned, either all eight exist or none.  Otherwise a row starts at any element and its last chunk may
+// be short.  Whole chunks are moved 16 bytes at a time all the same: global accesses of this target need the
+// element's alignment alone.  A short chunk is moved in pieces of 4, 2 and 1 elements, which stay where the loads put
+// them until the row is used (unpack8), so that nothing waits for them before.  At 16384 x 2047 bf16, us forward and
+// backward: element by element 79 and 179, whole chunks wide 38 and 101, short ones in pieces 34 and 46.
 template <bool BF16>
-struct Raw8;
-template <>
-struct Raw8<true> {
-  u32x4 w;
+struct Raw8 {
+  u32x4 w[BF16 ? 1 : 2];
 };
-template <>
-struct Raw8<false> {
-  u32x4 w[2];
-};
+
+// memory vectors of element alignment
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_a4 __attribute__((aligned(4)));
+typedef uint32_t u32_a2 __attribute__((aligned(2)));
 
 template <bool BF16, bool VEC>
 __device__ __forceinline__ Raw8<BF16> load8(const void* base, int64_t at, int nv) {
   Raw8<BF16> r;
-  if constexpr (BF16) {
+  r.w[0] = u32x4{0u, 0u, 0u, 0u};
+  if constexpr (!BF16) r.w[1] = u32x4{0u, 0u, 0u, 0u};
+  if constexpr (VEC) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(base) + at * (BF16 ? 2 : 4));
+    if (nv > 0) {
+      r.w[0] = p[0];
+      if constexpr (!BF16) r.w[1] = p[1];
+    }
+  } else if constexpr (BF16) {
     const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-    r.w = u32x4{0u, 0u, 0u, 0u};
-    if constexpr (VEC) {
-      if (nv > 0) r.w = *reinterpret_cast<const u32x4*>(p);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < nv) r.w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+    if (nv == 8) {
+      r.w[0] = *reinterpret_cast<const u32x4_a2*>(p);
+    } else if (nv > 0) {
+      if (nv & 4) {
+        const u32x2 v = *reinterpret_cast<const u32x2_a2*>(p);
+        r.w[0].x = v.x;
+        r.w[0].y = v.y;
+      }
+      if (nv & 2) r.w[0].z = *reinterpret_cast<const u32_a2*>(p + (nv & 4));
+      if (nv & 1) r.w[0].w = p[nv & 6];
     }
   } else {
     const uint32_t* p = static_cast<const uint32_t*>(base) + at;
-    r.w[0] = r.w[1] = u32x4{0u, 0u, 0u, 0u};
-    if constexpr (VEC) {
-      if (nv > 0) {
-        r.w[0] = *reinterpret_cast<const u32x4*>(p);
-        r.w[1] = *reinterpret_cast<const u32x4*>(p + 4);
+    if (nv == 8) {
+      r.w[0] = *reinterpret_cast<const u32x4_a4*>(p);
+      r.w[1] = *reinterpret_cast<const u32x4_a4*>(p + 4);
+    } else if (nv > 0) {
+      if (nv & 4) r.w[0] = *reinterpret_cast<const u32x4_a4*>(p);
+      if (nv & 2) {
+        const u32x2 v = *reinterpret_cast<const u32x2_a4*>(p + (nv & 4));
+        r.w[1].x = v.x;
+        r.w[1].y = v.y;
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < nv) r.w[j >> 2][j & 3] = p[j];
+      if (nv & 1) r.w[1].z = p[nv & 6];
     }
   }
   return r;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void unpack8(const Raw8<BF16>& r, float v[8]) {
+// The eight values, zero where there is no column.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void unpack8(const Raw8<BF16>& r, int nv, float v[8]) {
   if constexpr (BF16) {
+    u32x4 w = r.w[0];
+    if (!VEC && nv < 8) {
+      const uint32_t t0 = (nv & 2) ? w.z : w.w, t1 = (nv & 2) ? w.w : 0u;
+      w = (nv & 4) ? u32x4{w.x, w.y, t0, t1} : u32x4{t0, t1, 0u, 0u};
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (j & 1) ? bf16_hi(r.w[j >> 1]) : bf16_lo(r.w[j >> 1]);
+    for (int j = 0; j < 8; ++j) v[j] = (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
   } else {
+    u32x4 lo = r.w[0], hi = r.w[1];
+    if (!VEC && nv < 8) {
+      hi = (nv & 2) ? u32x4{hi.x, hi.y, hi.z, 0u} : u32x4{hi.z, 0u, 0u, 0u};
+      if (!(nv & 4)) {
+        lo = hi;
+        hi = u32x4{0u, 0u, 0u, 0u};
+      }
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r.w[j >> 2][j & 3]);
+    for (int j = 0; j < 4; ++j) {
+      v[j] = __uint_as_float(lo[j]);
+      v[j + 4] = __uint_as_float(hi[j]);
+    }
   }
 }
 
-// NT: past the caches.  Measured at 16384 x 2048 bf16 with inputs in rotation: the forward pass 23.2 us with
-// such stores and 25.4 without (they leave the memory-side cache to x), the backward pass 42.0 and 38.9 (its
-// inputs exceed that cache).
-template <bool NT, typename V>
-__device__ __forceinline__ void put(V v, V* p) {
-  if constexpr (NT)
-    __builtin_nontemporal_store(v, p);
-  else
-    *p = v;
-}
-
+// NT: past the caches, for aligned bf16 rows (where a store instruction fills whole lines).  Measured at
+// 16384 x 2048 bf16 with inputs in rotation: the forward pass 23.2 us with such stores and 25.4 without (they
+// leave the memory-side cache to x), the backward pass 42.0 and 38.9 (its inputs exceed that cache).
 template <bool BF16, bool VEC, bool NT>
 __device__ __forceinline__ void store8(void* base, int64_t at, int nv, const float v[8]) {
   if constexpr (BF16) {
     const u32x4 o = {bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
     uint16_t* p = static_cast<uint16_t*>(base) + at;
     if constexpr (VEC) {
-      if (nv > 0) put<NT>(o, reinterpret_cast<u32x4*>(p));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < nv) p[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+      if (nv > 0) {
+        if constexpr (NT)
+          __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(p));
+        else
+          *reinterpret_cast<u32x4*>(p) = o;
+      }
+    } else if (nv == 8) {
+      *reinterpret_cast<u32x4_a2*>(p) = o;
+    } else if (nv > 0) {
+      if (nv & 4) *reinterpret_cast<u32x2_a2*>(p) = u32x2{o.x, o.y};
+      const uint32_t two = (nv & 4) ? o.z : o.x, three = (nv & 4) ? o.w : o.y;
+      if (nv & 2) *reinterpret_cast<u32_a2*>(p + (nv & 4)) = two;
+      if (nv & 1) p[nv & 6] = (uint16_t)((nv & 2) ? three : two);
     }
   } else {
     float* p = static_cast<float*>(base) + at;
+    const u32x4 lo = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+    const u32x4 hi = __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]});
     if constexpr (VEC) {
       if (nv > 0) {
-        put<NT>(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
-        put<NT>(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(p + 4));
+        reinterpret_cast<u32x4*>(p)[0] = lo;
+        reinterpret_cast<u32x4*>(p)[1] = hi;
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < nv) p[j] = v[j];
+    } else if (nv == 8) {
+      *reinterpret_cast<u32x4_a4*>(p) = lo;
+      *reinterpret_cast<u32x4_a4*>(p + 4) = hi;
+    } else if (nv > 0) {
+      if (nv & 4) *reinterpret_cast<u32x4_a4*>(p) = lo;
+      const u32x4 t = (nv & 4) ? hi : lo;
+      if (nv & 2) *reinterpret_cast<u32x2_a4*>(p + (nv & 4)) = u32x2{t.x, t.y};
+      if (nv & 1) p[nv & 6] = __uint_as_float((nv & 2) ? t.z : t.x);
     }
   }
 }
@@ -121,9 +161,9 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int nv, const flo
 __device__ __forceinline__ void load_vec8(const void* base, bool bf16, bool aligned, int col, int nv, float v[8]) {
   if (aligned && nv == 8) {
     if (bf16)
-      unpack8<true>(load8<true, true>(base, col, 8), v);
+      unpack8<true, true>(load8<true, true>(base, col, 8), 8, v);
     else
-      unpack8<false>(load8<false, true>(base, col, 8), v);
+      unpack8<false, true>(load8<false, true>(base, col, 8), 8, v);
     return;
   }
 #pragma unroll
@@ -143,28 +183,31 @@ __device__ __forceinline__ float dpp_add(float v) {
   return v + __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum over the 16, 32 or 64 lanes of a wave that share a row (N; more: over the wave).
+template <int N>
+__device__ __forceinline__ float lanes_sum(float v) {
   v = dpp_add<kDppQuadXor1>(v);
   v = dpp_add<kDppQuadXor2>(v);
   v = dpp_add<kDppRowHalfMirror>(v);
   v = dpp_add<kDppRowMirror>(v);
-  v += __shfl_xor(v, 16);
-  v += __shfl_xor(v, 32);
+  if constexpr (N > 16) v += __shfl_xor(v, 16);
+  if constexpr (N > 32) v += __shfl_xor(v, 32);
   return v;
 }
 
-// Sum over a team of WPR waves; every lane gets it.  `slot` is one of two LDS rows used in turn, so a
+// Sum over a team of LPR lanes; every lane gets it.  `slot` is one of two LDS rows used in turn, so a
 // wave that runs ahead into the next sum does not overwrite what a slower one still reads (the
 // barrier of the next sum is between them).
-template <int WPR, int WAVES>
-__device__ __forceinline__ float team_sum(float v, float (*red)[WAVES], int slot, int wave) {
-  v = wave_sum(v);
-  if constexpr (WPR > 1) {
+template <int LPR, int WAVES>
+__device__ __forceinline__ float team_sum(float v, float (*red)[WAVES], int slot) {
+  v = lanes_sum<LPR>(v);
+  if constexpr (LPR > 64) {
+    const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) red[slot][wave] = v;
     __syncthreads();
     v = 0.f;
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) v += red[slot][(wave / WPR) * WPR + w];
+    for (int w = 0; w < LPR / 64; ++w) v += red[slot][wave / (LPR / 64) * (LPR / 64) + w];
   }
   return v;
 }
@@ -182,7 +225,7 @@ __device__ __forceinline__ void tile_scale32(float amax, float& s, float& r) {
 template <bool BF16>
 __device__ __forceinline__ void norm8(const Raw8<BF16>& raw, float rstd, float shift, const float g[8], const float b[8],
                                       float y[8]) {
-  unpack8<BF16>(raw, y);
+  unpack8<BF16, true>(raw, 8, y);
 #pragma unroll
   for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(__builtin_fmaf(y[j], rstd, shift), g[j], b[j]);
 }
@@ -203,22 +246,21 @@ __device__ __forceinline__ float row16_maxf(float v) {   // v >= 0
 }
 
 // ---------------------------------------------------------------------------------------------------
-// Forward.  A team of WPR waves takes a row, each thread ITER chunks of eight columns, chunk i of team
-// thread t at column 8 (64 WPR i + t): 16-byte loads that are contiguous over a wave, and 16 lanes
-// hold one 128-column group.  A team takes rows_per_team consecutive rows (the 32-row run of a
+// Forward.  A team of LPR lanes takes a row (16 lanes, so that a wave takes four short rows, up to eight waves), each
+// lane ITER chunks of eight columns, chunk i of team lane t at column 8 (LPR i + t): 16-byte loads that are
+// contiguous over a team, and 16 lanes hold one 128-column group.  A team takes rows_per_team consecutive rows (the 32-row run of a
 // workgroup then fills whole lines of the row-wise scale and statistics arrays) and loads the next
 // row before it works on the present one.
 // WHAT: 0 y, 1 codes and scales, 2 the statistics alone (first launch of the dual form).
 // ---------------------------------------------------------------------------------------------------
-template <bool BF16, bool VEC, int WPR, int ITER, int WHAT>
-__global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs a) {
-  constexpr int kWaves = WPR > 4 ? WPR : 4;
-  constexpr int kTeams = kWaves / WPR;
-  constexpr int kTeamThreads = 64 * WPR;
+template <bool BF16, bool VEC, int LPR, int ITER, int WHAT>
+__global__ __launch_bounds__(LPR > 256 ? LPR : 256) void norm_kernel(NormArgs a) {
+  constexpr int kThreads = LPR > 256 ? LPR : 256;
+  constexpr int kWaves = kThreads / 64;
+  constexpr int kTeams = kThreads / LPR;
   __shared__ float red[2][kWaves];
-  const int wave = threadIdx.x >> 6;
-  const int team = wave / WPR;
-  const int tt = threadIdx.x - team * kTeamThreads;
+  const int team = threadIdx.x / LPR;
+  const int tt = threadIdx.x % LPR;
   const int64_t row0 = ((int64_t)blockIdx.x * kTeams + team) * a.rows_per_team;
 
   int col[ITER], nv[ITER];
@@ -226,7 +268,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs
   Raw8<BF16> next[ITER];
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
-    col[i] = 8 * (kTeamThreads * i + tt);
+    col[i] = 8 * (LPR * i + tt);
     nv[i] = a.C - col[i] < 0 ? 0 : (a.C - col[i] > 8 ? 8 : a.C - col[i]);
     next[i] = load8<BF16, VEC>(a.x, row0 * a.ldx + col[i], row0 < a.T ? nv[i] : 0);
   }
@@ -247,7 +289,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
       cur[i] = next[i];
-      unpack8<BF16>(cur[i], v[i]);
+      unpack8<BF16, VEC>(cur[i], nv[i], v[i]);
     }
     if (k + 1 < a.rows_per_team) {
 #pragma unroll
@@ -261,25 +303,26 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs
       for (int i = 0; i < ITER; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum += v[i][j];   // missing columns were loaded as zero
-      mean = team_sum<WPR, kWaves>(sum, red, 0, wave) * inv_c;
+      mean = team_sum<LPR, kWaves>(sum, red, 0) * inv_c;
     }
     float sq = 0.f;
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
       float part = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[i][j] -= mean;
-        if constexpr (VEC)
-          part = __builtin_fmaf(v[i][j], v[i][j], part);
-        else
-          part = j < nv[i] ? __builtin_fmaf(v[i][j], v[i][j], part) : part;
+      for (int j = 0; j < 8; ++j) v[i][j] -= mean;
+      if (VEC || nv[i] == 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) part = __builtin_fmaf(v[i][j], v[i][j], part);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 7; ++j) part = j < nv[i] ? __builtin_fmaf(v[i][j], v[i][j], part) : part;
       }
       sq += nv[i] > 0 ? part : 0.f;
     }
     // (an RMS norm has this sum alone, so it takes the LDS rows in turn from row to row)
     const float rstd =
-        1.0f / __builtin_sqrtf(team_sum<WPR, kWaves>(sq, red, a.layer ? 1 : (k & 1), wave) * inv_c + a.eps);
+        1.0f / __builtin_sqrtf(team_sum<LPR, kWaves>(sq, red, a.layer ? 1 : (k & 1)) * inv_c + a.eps);
     if (ok && tt == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -292,7 +335,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : 256) void norm_kernel(NormArgs
 #pragma unroll
           for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(v[i][j] * rstd, g[i][j], b[i][j]);
           store8<BF16, VEC, true>(a.y, row * a.ldy + col[i], ok ? nv[i] : 0, y);
-        } else {
+        } else if constexpr (VEC) {
           norm8<BF16>(cur[i], rstd, -mean * rstd, g[i], b[i], y);
           float m = 0.f;
 #pragma unroll
@@ -417,7 +460,7 @@ __global__ __launch_bounds__(kDualThreads) void norm_dual_kernel(NormArgs a, int
 }
 
 // ---------------------------------------------------------------------------------------------------
-// Backward.  Eight waves per workgroup, teams of WPR waves with a row each; thread columns as in the
+// Backward.  Eight waves per workgroup, teams of LPR lanes with a row each; a lane's columns as in the
 // forward kernel.  The weight's and bias's gradient of a thread's columns are summed in registers
 // over the team's rows, then over the workgroup's teams through LDS, and written as the workgroup's
 // partial sums; norm_bwd_reduce_kernel adds those in order.
@@ -425,23 +468,21 @@ __global__ __launch_bounds__(kDualThreads) void norm_dual_kernel(NormArgs a, int
 constexpr int kBwdThreads = 512;
 constexpr int kBwdWaves = kBwdThreads / 64;
 
-template <bool BF16, bool VEC, int WPR, int ITER>
+template <bool BF16, bool VEC, int LPR, int ITER>
 __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, int rows_per_team, bool direct) {
-  constexpr int kTeams = kBwdWaves / WPR;
-  constexpr int kTeamThreads = 64 * WPR;
-  constexpr int kWidth = 8 * kTeamThreads * ITER;
+  constexpr int kTeams = kBwdThreads / LPR;
+  constexpr int kWidth = 8 * LPR * ITER;
   __shared__ float red[2][2][kBwdWaves];
   __shared__ float join[kTeams > 1 ? kTeams * kWidth : 4];
-  const int wave = threadIdx.x >> 6;
-  const int team = wave / WPR;
-  const int tt = threadIdx.x - team * kTeamThreads;
+  const int team = threadIdx.x / LPR;
+  const int tt = threadIdx.x % LPR;
   const int64_t stride = (int64_t)gridDim.x * kTeams;
 
   int col[ITER], nv[ITER];
   float g[ITER][8], dg[ITER][8], db[ITER][8];
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
-    col[i] = 8 * (kTeamThreads * i + tt);
+    col[i] = 8 * (LPR * i + tt);
     nv[i] = a.C - col[i] < 0 ? 0 : (a.C - col[i] > 8 ? 8 : a.C - col[i]);
     load_vec8(a.gamma, a.w_bf16, aligned16(a.gamma), col[i], nv[i], g[i]);
 #pragma unroll
@@ -469,8 +510,8 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, in
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-      unpack8<BF16>(nx[i], xh[i]);
-      unpack8<BF16>(ny[i], d[i]);
+      unpack8<BF16, VEC>(nx[i], nv[i], xh[i]);
+      unpack8<BF16, VEC>(ny[i], nv[i], d[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // a column that does not exist has dy = 0 and weight 0: it adds nothing to any sum
@@ -483,20 +524,21 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, in
       }
     }
     if (k + 1 < rows_per_team) fetch(row + stride);
-    s1 = wave_sum(s1);
-    s2 = wave_sum(s2);
-    if constexpr (WPR > 1) {
+    s1 = lanes_sum<LPR>(s1);
+    s2 = lanes_sum<LPR>(s2);
+    if constexpr (LPR > 64) {
+      constexpr int kTeamWaves = LPR / 64;
       const int slot = k & 1;
       if ((threadIdx.x & 63) == 0) {
-        red[slot][0][wave] = s1;
-        red[slot][1][wave] = s2;
+        red[slot][0][threadIdx.x >> 6] = s1;
+        red[slot][1][threadIdx.x >> 6] = s2;
       }
       __syncthreads();
       s1 = s2 = 0.f;
 #pragma unroll
-      for (int w = 0; w < WPR; ++w) {
-        s1 += red[slot][0][team * WPR + w];
-        s2 += red[slot][1][team * WPR + w];
+      for (int w = 0; w < kTeamWaves; ++w) {
+        s1 += red[slot][0][team * kTeamWaves + w];
+        s2 += red[slot][1][team * kTeamWaves + w];
       }
     }
     s1 = a.layer ? s1 * inv_c : 0.f;
@@ -587,44 +629,50 @@ inline bool vec_row(const void* p, int64_t ld, int64_t es) {
 template <bool BF16, bool VEC, int WHAT>
 hipError_t launch_fwd(NormArgs a, hipStream_t st) {
   // The layout over threads goes by C alone, so every form sums a row in the same order.
-  auto go = [&](auto kernel, int wpr) {
-    const int waves = wpr > 4 ? wpr : 4, teams = waves / wpr;
-    // rows per team: 8 for long inputs, so that a workgroup's 32 rows fill whole lines of the row-wise
-    // arrays; one row where the input would not fill the card otherwise
-    int64_t r = std::max<int64_t>(1, std::min<int64_t>(8, a.T / (2048 / wpr)));
+  auto go = [&](auto kernel, int lpr) {
+    const int threads = lpr > 256 ? lpr : 256, teams = threads / lpr;
+    // rows per team: 8 for long inputs, so that a workgroup's rows fill whole lines of the row-wise
+    // arrays; one row where the input would not give the card 2048 waves otherwise
+    const int64_t r = std::max<int64_t>(1, std::min<int64_t>(8, a.T / (131072 / lpr)));
     a.rows_per_team = (int)r;
     const int64_t blocks = (a.T + teams * r - 1) / (teams * r);
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(64 * waves), 0, st, a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), 0, st, a);
     return hipGetLastError();
   };
-  if (a.C <= 512) return go(norm_kernel<BF16, VEC, 1, 1, WHAT>, 1);
-  if (a.C <= 1024) return go(norm_kernel<BF16, VEC, 1, 2, WHAT>, 1);
-  if (a.C <= 2048) return go(norm_kernel<BF16, VEC, 2, 2, WHAT>, 2);
-  if (a.C <= 4096) return go(norm_kernel<BF16, VEC, 4, 2, WHAT>, 4);
-  if (a.C <= 8192) return go(norm_kernel<BF16, VEC, 8, 2, WHAT>, 8);
-  return go(norm_kernel<BF16, VEC, 8, 4, WHAT>, 8);
+  if (a.C <= 128) return go(norm_kernel<BF16, VEC, 16, 1, WHAT>, 16);
+  if (a.C <= 256) return go(norm_kernel<BF16, VEC, 32, 1, WHAT>, 32);
+  if (a.C <= 512) return go(norm_kernel<BF16, VEC, 64, 1, WHAT>, 64);
+  if (a.C <= 1024) return go(norm_kernel<BF16, VEC, 64, 2, WHAT>, 64);
+  if (a.C <= 2048) return go(norm_kernel<BF16, VEC, 128, 2, WHAT>, 128);
+  if (a.C <= 4096) return go(norm_kernel<BF16, VEC, 256, 2, WHAT>, 256);
+  if (a.C <= 8192) return go(norm_kernel<BF16, VEC, 512, 2, WHAT>, 512);
+  return go(norm_kernel<BF16, VEC, 512, 4, WHAT>, 512);
 }
 
-// waves per row of the backward kernel; its rows per workgroup and step are kBwdWaves / this
-int bwd_wpr(int64_t C) { return C <= 1024 ? 1 : C <= 2048 ? 2 : C <= 4096 ? 4 : 8; }
+// lanes per row of the backward kernel; it takes kBwdThreads / this rows per workgroup and step
+int bwd_lpr(int64_t C) {
+  return C <= 128 ? 16 : C <= 256 ? 32 : C <= 1024 ? 64 : C <= 2048 ? 128 : C <= 4096 ? 256 : 512;
+}
 
 template <bool BF16, bool VEC>
 hipError_t launch_bwd(const NormBwdArgs& a, hipStream_t st) {
   const int blocks = norm_bwd_blocks(a.T, a.C);
-  const int teams = kBwdWaves / bwd_wpr(a.C);
+  const int teams = kBwdThreads / bwd_lpr(a.C);
   const int rows = (int)((a.T + (int64_t)blocks * teams - 1) / ((int64_t)blocks * teams));
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kBwdThreads), 0, st, a, rows, blocks == 1);
     return hipGetLastError();
   };
   hipError_t e;
-  if (a.C <= 512) e = go(norm_bwd_kernel<BF16, VEC, 1, 1>);
-  else if (a.C <= 1024) e = go(norm_bwd_kernel<BF16, VEC, 1, 2>);
-  else if (a.C <= 2048) e = go(norm_bwd_kernel<BF16, VEC, 2, 2>);
-  else if (a.C <= 4096) e = go(norm_bwd_kernel<BF16, VEC, 4, 2>);
-  else if (a.C <= 8192) e = go(norm_bwd_kernel<BF16, VEC, 8, 2>);
-  else e = go(norm_bwd_kernel<BF16, VEC, 8, 4>);
+  if (a.C <= 128) e = go(norm_bwd_kernel<BF16, VEC, 16, 1>);
+  else if (a.C <= 256) e = go(norm_bwd_kernel<BF16, VEC, 32, 1>);
+  else if (a.C <= 512) e = go(norm_bwd_kernel<BF16, VEC, 64, 1>);
+  else if (a.C <= 1024) e = go(norm_bwd_kernel<BF16, VEC, 64, 2>);
+  else if (a.C <= 2048) e = go(norm_bwd_kernel<BF16, VEC, 128, 2>);
+  else if (a.C <= 4096) e = go(norm_bwd_kernel<BF16, VEC, 256, 2>);
+  else if (a.C <= 8192) e = go(norm_bwd_kernel<BF16, VEC, 512, 2>);
+  else e = go(norm_bwd_kernel<BF16, VEC, 512, 4>);
   if (e != hipSuccess || blocks == 1) return e;
   hipLaunchKernelGGL(norm_bwd_reduce_kernel, dim3((unsigned)((a.C + 15) / 16), a.dbeta ? 2 : 1), dim3(256), 0, st,
                      a.partial, blocks, a.C, a.dgamma, a.dbeta, a.accumulate);
@@ -660,7 +708,7 @@ hipError_t launch_norm_quant_dual(NormArgs a, hipStream_t st) {
 
 int norm_bwd_blocks(int64_t T, int64_t C) {
   if (T <= 0 || C <= 0) return 0;
-  const int teams = kBwdWaves / bwd_wpr(C);
+  const int teams = kBwdThreads / bwd_lpr(C);
   return (int)std::min<int64_t>(256, (T + 2 * teams - 1) / (2 * teams));
 }
 
