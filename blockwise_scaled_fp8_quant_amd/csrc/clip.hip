@@ -27,10 +27,12 @@ constexpr int kThreads = 256;
 constexpr int kVecs = 4;
 constexpr int kMaxBlocks = 2048;
 
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+
 struct JobDesc {
   const uint8_t* src;
   uint8_t* dst;
-  int64_t n;          // elements; the sign bit of `first` carries the type
+  int64_t n;          // elements
   uint32_t first;     // first chunk of the job in the launch
   uint32_t bf16;
 };
@@ -184,8 +186,12 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(JobTable t, const 
       for (int d = 0; d < 4; ++d)
         o[d] = j.bf16 ? bf16x2_rne(bf16_lo(w[k][d]) * coef, bf16_hi(w[k][d]) * coef)
                       : __float_as_uint(__uint_as_float(w[k][d]) * coef);
-      if (same && p.lo == 0 && p.hi == per) {
-        __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(j.dst + p.first * es));
+      if (p.lo == 0 && p.hi == per) {
+        uint8_t* d = j.dst + p.first * es;
+        if (same)
+          __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(d));
+        else   // whole vectors of the input at another alignment: global stores need the element's alone
+          *reinterpret_cast<u32x4_a2*>(d) = o;
       } else {
         for (int e = p.lo; e < p.hi; ++e) {
           const int d = per == 8 ? e >> 1 : e;

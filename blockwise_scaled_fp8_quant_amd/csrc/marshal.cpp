@@ -356,6 +356,8 @@ PyObject* layer_norm_backward(PyObject* const* a) {
 }
 
 // The jobs of a list of gradients and, where given, of their outputs.  (The lists are the caller's and hold the tensors.)
+// A gradient fills its range of memory in any order of its dimensions (contiguous, or the transpose of that), which
+// is all that its norm and scaling need; its output then has the same strides.
 std::vector<puro_grad_job> grad_jobs(const Call& c, PyObject* grads, PyObject* outs) {
   if (!PyList_Check(grads) && !PyTuple_Check(grads)) type_error("grads: expected a list of tensors");
   if (outs != Py_None && !PyList_Check(outs) && !PyTuple_Check(outs)) type_error("outs: expected a list of tensors");
@@ -369,7 +371,9 @@ std::vector<puro_grad_job> grad_jobs(const Call& c, PyObject* grads, PyObject* o
     at::ScalarType st;
     const std::string what = name("grads");
     const int code = dtype_code(o, what, st);
-    const at::Tensor& g = c.whole(o, what, st, nullptr);
+    const at::Tensor& g = c.tensor(o, what, st, nullptr);
+    const bool whole = g.is_contiguous();
+    if (!whole && !g.is_non_overlapping_and_dense()) value_error(what + ": must be contiguous");
     puro_grad_job& j = jobs[(size_t)i];
     j.src = g.data_ptr();
     j.dst = g.data_ptr();
@@ -377,7 +381,9 @@ std::vector<puro_grad_job> grad_jobs(const Call& c, PyObject* grads, PyObject* o
     j.dtype = code;
     if (outs != Py_None) {
       const Shape shape = g.sizes().vec();
-      j.dst = c.whole(PySequence_Fast_GET_ITEM(outs, i), name("outs"), st, &shape).data_ptr();
+      const at::Tensor& d = c.tensor(PySequence_Fast_GET_ITEM(outs, i), name("outs"), st, &shape);
+      if (whole ? !d.is_contiguous() : d.strides() != g.strides()) value_error(name("outs") + ": must have the gradient's layout");
+      j.dst = d.data_ptr();
     }
   }
   return jobs;

@@ -129,14 +129,15 @@ def puro_layer_norm_backward(dy, x, weight, mean, rstd, kind: int = LAYER_NORM, 
 
 
 def puro_grad_norm(grads, norm=None, workspace=None, stream=None):
-    """norm (fp32, one value, on the GPU): the square root of the sum of all squares of a list of contiguous
-    bf16 or fp32 tensors."""
+    """norm (fp32, one value, on the GPU): the square root of the sum of all squares of a list of bf16 or fp32
+    tensors, each contiguous or dense in another order of its dimensions."""
     return _on(stream, _marshal.clip_grad_norm)(list(grads), None, None, norm, workspace)
 
 
 def puro_clip_grad_norm(grads, max_norm: float, outs=None, norm=None, workspace=None, stream=None):
-    """(norm, outs): the global norm of a list of contiguous bf16 or fp32 tensors, and the tensors times
-    min(1, max_norm / (norm + 1e-6)) -- in place (outs is then grads), or into the tensors given as outs."""
+    """(norm, outs): the global norm of a list of tensors as puro_grad_norm takes them, and the tensors times
+    min(1, max_norm / (norm + 1e-6)) -- in place (outs is then grads), or into the tensors given as outs, of the same
+    types, shapes and layouts."""
     grads = list(grads)
     if max_norm is None:
         raise TypeError("max_norm: expected a number")

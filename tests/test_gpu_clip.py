@@ -111,7 +111,11 @@ def test_refusals(P):
     t = torch()
     g = t.ones(64, 64, device="cuda")
     with pytest.raises(ValueError):
-        P.puro_grad_norm([g.t()])
+        P.puro_grad_norm([g[:, :32]])
+    with pytest.raises(ValueError):
+        P.puro_grad_norm([g[:1].expand(64, 64)])
+    with pytest.raises(ValueError):
+        P.puro_clip_grad_norm([g.t()], 1.0, outs=[t.empty_like(g).contiguous()])
     with pytest.raises(ValueError):
         P.puro_clip_grad_norm([g], 1.0, outs=[t.ones(64, device="cuda")])
     with pytest.raises(TypeError):
@@ -129,6 +133,17 @@ def test_refusals(P):
     with pytest.raises(ValueError):
         P.puro_scale_by_norm([g], 1.0, t.ones(2, device="cuda"))
     assert (g == 1).all()
+
+
+def test_other_orders_of_dimensions(P):
+    """A dense tensor in another order of its dimensions: the same norm and the same elements."""
+    t = torch()
+    g = t.randn((3, 50, 70), device="cuda").permute(2, 0, 1)
+    n, (o,) = P.puro_clip_grad_norm([g], 0.5, outs=[t.empty_like(g)])
+    n2, (o2,) = P.puro_clip_grad_norm([g.contiguous()], 0.5)
+    assert float(n) == float(n2) and t.equal(o, o2)
+    P.puro_clip_grad_norm([g], 0.5)
+    assert t.equal(g, o)
 
 
 def test_graph_and_stream(P):
