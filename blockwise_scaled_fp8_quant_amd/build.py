@@ -78,7 +78,7 @@ def _link_marshal(obj: str) -> None:
     # torch's libraries are those that importing torch, which comes first, has loaded: no path to them is kept
     tmp = MARSHAL + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", PKG, "-lpuro_fp8", "-Wl,-rpath,$ORIGIN",
-           "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+           "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")

@@ -260,6 +260,7 @@ hipError_t launch_gemm_rows(int64_t M, int64_t N, int64_t K, const uint8_t* A, i
                       static_cast<uint8_t*>(C) + lead * ldc * (out_bf16 ? 2 : 4), ldc};
   if (rows <= 16) return by_strips<1>(a, out_bf16, st);
   if (rows <= 32) return by_strips<2>(a, out_bf16, st);
+  if (rows <= 48) return by_strips<3>(a, out_bf16, st);   // (37 x 4096 x 2048: 4.9 us, 5.4 as 64 rows)
   return by_strips<4>(a, out_bf16, st);
 }
 

@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -130,7 +131,8 @@ class Call {
   }
 
   at::Tensor make(const Shape& shape, at::ScalarType dtype) const {
-    return at::empty(shape, at::TensorOptions().dtype(dtype).device(at::Device(at::kCUDA, (c10::DeviceIndex)dev_)));
+    // torch.empty without its dispatch, which costs as much as the allocation
+    return at::Tensor(at::detail::empty_cuda(shape, dtype, at::Device(at::kCUDA, (c10::DeviceIndex)dev_), c10::nullopt));
   }
 
   at::Tensor out_rows(PyObject* o, const char* what, at::ScalarType dtype, const Shape& shape, int64_t& ld) const {

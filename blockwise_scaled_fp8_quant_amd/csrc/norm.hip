@@ -706,10 +706,16 @@ hipError_t launch_norm_quant_dual(NormArgs a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// One workgroup per CU, but no more than there are rows for its teams, and beyond 64 no more than one for 8 rows:
+// every workgroup writes and the second launch reads 8 bytes per column, which at 8 rows (6 bytes per element and
+// row in bf16) is a third of the pass.  A single one, without a second launch, up to two rows per team.  Measured, us:
+// 64 x 2048 7.1 (7.9 with two rows per team at least); 1027 x 4096 14.6 with 128 workgroups, 18.0 with 256; 16 x 1000
+// 5.1 alone, 6.7 in two.
 int norm_bwd_blocks(int64_t T, int64_t C) {
   if (T <= 0 || C <= 0) return 0;
-  const int teams = kBwdThreads / bwd_lpr(C);
-  return (int)std::min<int64_t>(256, (T + 2 * teams - 1) / (2 * teams));
+  const int64_t teams = kBwdThreads / bwd_lpr(C);
+  if (T <= 2 * teams) return 1;
+  return (int)std::min<int64_t>(std::min<int64_t>(256, (T + teams - 1) / teams), std::max<int64_t>(64, (T + 7) / 8));
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t st) {
