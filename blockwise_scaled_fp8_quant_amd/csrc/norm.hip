@@ -248,10 +248,12 @@ __device__ __forceinline__ float row16_maxf(float v) {   // v >= 0
 // ---------------------------------------------------------------------------------------------------
 // Forward.  A team of LPR lanes takes a row (16 lanes, so that a wave takes four short rows, up to eight waves), each
 // lane ITER chunks of eight columns, chunk i of team lane t at column 8 (LPR i + t): 16-byte loads that are
-// contiguous over a team, and 16 lanes hold one 128-column group.  A team takes rows_per_team consecutive rows (the 32-row run of a
-// workgroup then fills whole lines of the row-wise scale and statistics arrays) and loads the next
-// row before it works on the present one.
+// contiguous over a team, and 16 lanes hold one 128-column group.  A team takes rows_per_team consecutive rows and loads the
+// next one before it works on the present one.
 // WHAT: 0 y, 1 codes and scales, 2 the statistics alone (first launch of the dual form).
+// Measured, 16384 x 2048 bf16: y 23.0 us (5.8 TB/s, a copy's rate), the statistics 12.0 (5.6 TB/s read); one row 2.9 us, its
+// two sums' chains and one trip to memory.  Two chunks per lane: with four (64 lanes a row) 168 registers leave three waves
+// per SIMD, 24.4 us.
 // ---------------------------------------------------------------------------------------------------
 template <bool BF16, bool VEC, int LPR, int ITER, int WHAT>
 __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void norm_kernel(NormArgs a) {
@@ -464,6 +466,7 @@ __global__ __launch_bounds__(kDualThreads) void norm_dual_kernel(NormArgs a, int
 // forward kernel.  The weight's and bias's gradient of a thread's columns are summed in registers
 // over the team's rows, then over the workgroup's teams through LDS, and written as the workgroup's
 // partial sums; norm_bwd_reduce_kernel adds those in order.
+// Measured, 16384 x 2048 bf16: 35.3 us (5.7 TB/s) + 4.7 for the joining; with four chunks per lane 40.4.
 // ---------------------------------------------------------------------------------------------------
 constexpr int kBwdThreads = 512;
 constexpr int kBwdWaves = kBwdThreads / 64;
@@ -631,9 +634,11 @@ hipError_t launch_fwd(NormArgs a, hipStream_t st) {
   // The layout over threads goes by C alone, so every form sums a row in the same order.
   auto go = [&](auto kernel, int lpr) {
     const int threads = lpr > 256 ? lpr : 256, teams = threads / lpr;
-    // rows per team: 8 for long inputs, so that a workgroup's rows fill whole lines of the row-wise
-    // arrays; one row where the input would not give the card 2048 waves otherwise
-    const int64_t r = std::max<int64_t>(1, std::min<int64_t>(8, a.T / (131072 / lpr)));
+    // rows per team: 4 for long inputs, so that the next row's loads hide behind this one and a workgroup's rows are runs of
+    // the row-wise arrays; one row where the input would not give the card 2048 waves otherwise.  (8 rows leave
+    // too few workgroups to share evenly: 16384 x 1024 bf16 15.3 us, 12.2 with 4; 3000 x 3000 10.2 and 9.2; 16384 x 2048
+    // 23.5 and 23.2.  2 rows: 36.0 us at 16384 x 2047, 32.4 with 4.)
+    const int64_t r = std::max<int64_t>(1, std::min<int64_t>(4, a.T / (131072 / lpr)));
     a.rows_per_team = (int)r;
     const int64_t blocks = (a.T + teams * r - 1) / (teams * r);
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
