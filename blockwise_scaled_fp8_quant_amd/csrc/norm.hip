@@ -221,7 +221,7 @@ __device__ __forceinline__ void tile_scale32(float amax, float& s, float& r) {
 
 // The norm of eight columns for the quantized forms: two FMAs per element, (x r - mu r) g + b, with
 // shift = -mu r.  (The tensor form subtracts the mean first: one rounding less where |mu| is many deviations.
-// Three bits of mantissa do not show it, and the dual form's second launch is bound by its vector instructions.)
+// Three bits of mantissa do not show it, and the dual form's second launch has many vector instructions.)
 template <bool BF16>
 __device__ __forceinline__ void norm8(const Raw8<BF16>& raw, float rstd, float shift, const float g[8], const float b[8],
                                       float y[8]) {
@@ -338,7 +338,7 @@ __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void norm_kernel(NormArgs a)
           for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(v[i][j] * rstd, g[i][j], b[i][j]);
           store8<BF16, VEC, true>(a.y, row * a.ldy + col[i], ok ? nv[i] : 0, y);
         } else if constexpr (VEC) {
-          norm8<BF16>(cur[i], rstd, -mean * rstd, g[i], b[i], y);
+          norm8<BF16>(cur[i], rstd, a.layer ? -mean * rstd : 0.f, g[i], b[i], y);
           float m = 0.f;
 #pragma unroll
           for (int j = 0; j < 8; j += 2) m = max3abs(m, y[j], y[j + 1]);
@@ -476,7 +476,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, in
   constexpr int kTeams = kBwdThreads / LPR;
   constexpr int kWidth = 8 * LPR * ITER;
   __shared__ float red[2][2][kBwdWaves];
-  __shared__ float join[kTeams > 1 ? kTeams * kWidth : 4];
+  __shared__ __attribute__((aligned(16))) float join[kTeams > 1 ? kTeams * kWidth : 4];
   const int team = threadIdx.x / LPR;
   const int tt = threadIdx.x % LPR;
   const int64_t stride = (int64_t)gridDim.x * kTeams;

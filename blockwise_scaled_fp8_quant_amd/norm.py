@@ -153,10 +153,12 @@ class Fp8NormLinear(torch.nn.Module):
 
     def forward(self, x, codes=None):
         n, w = self.norm, self.linear.weight
-        if codes is None and (torch.is_grad_enabled() or (x.numel() // max(w.shape[1], 1)) % 128 == 0):
-            return Fp8NormLinearFunction.apply(x, n.weight, n.bias, w, n.eps, n.kind)
+        if x.shape[-1] != w.shape[1]:
+            raise ValueError(f"x has {x.shape[-1]} features, weight expects {w.shape[1]}")
         if torch.is_grad_enabled():
-            raise ValueError("codes: a weight quantized beforehand is for use without gradients (torch.no_grad)")
+            if codes is not None:
+                raise ValueError("codes: a weight quantized beforehand is for use without gradients (torch.no_grad)")
+            return Fp8NormLinearFunction.apply(x, n.weight, n.bias, w, n.eps, n.kind)
         wq, ws = self.quantize_weight() if codes is None else codes
         xq, xs = puro_layer_norm_quant(_rows(x, w.shape[1]), n.weight, n.bias, eps=n.eps, kind=n.kind)
         return puro_gemm_rows(xq, xs, wq, ws).view(*x.shape[:-1], w.shape[0])

@@ -40,7 +40,8 @@ enum { PURO_NORM_LAYER = 0, PURO_NORM_RMS = 1 };
  * Mean and variance are taken in fp32 from the row held in registers (variance of the differences
  * from the mean, not of squares), y is rounded once.  Rows need only element alignment (2 or 4
  * bytes, any ldx >= C); 16-byte aligned rows with C % 8 == 0 take the fast path.
- * A row holding a NaN or an infinity gives NaN in that row alone.  C > 16384: PURO_ERR_UNSUPPORTED.
+ * A NaN or an infinity stays in its row (a layer norm's whole row becomes NaN).  Squares are fp32: beyond about 1e17
+ * of |x - mu| their sum leaves its range, rstd is 0 and y is bias.  C > 16384: PURO_ERR_UNSUPPORTED.
  */
 int puro_layer_norm(int kind, int x_dtype, const void* x, int64_t T, int64_t C, int64_t ldx, int w_dtype,
                     const void* weight, const void* bias, float eps, void* y, int64_t ldy, float* mean, float* rstd,

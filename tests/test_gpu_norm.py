@@ -371,6 +371,27 @@ def test_norm_on_another_stream_and_in_a_graph(P):
             assert t.equal(a, c), k
 
 
+def test_two_streams_at_once(P):
+    """Calls on two streams that are not ordered, each with outputs and a workspace of its own."""
+    t = torch()
+    work = []
+    for k in range(2):
+        x, w, b = inputs(2000, 2048, t.bfloat16, t.bfloat16, 0, k)
+        dy = t.randn_like(x)
+        y, m, r = P.puro_layer_norm(x, w, b)
+        work.append((x, w, b, dy, m, r, y, P.puro_layer_norm_backward(dy, x, w, m, r)))
+    streams = [t.cuda.Stream(), t.cuda.Stream()]
+    t.cuda.synchronize()
+    got = []
+    for n in range(10):
+        for s, (x, w, b, dy, m, r, y, want) in zip(streams, work):
+            got.append((P.puro_layer_norm(x, w, b, stream=s)[0], y))
+            got += list(zip(P.puro_layer_norm_backward(dy, x, w, m, r, stream=s), want))
+    t.cuda.synchronize()
+    for a, c in got:
+        assert t.equal(a, c)
+
+
 def test_norm_binding_refusals(P):
     t = torch()
     x, w, b = inputs(4, 128, t.bfloat16, t.bfloat16, 0, 1)

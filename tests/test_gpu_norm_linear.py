@@ -96,10 +96,19 @@ def test_serving_any_number_of_rows(P):
             assert y.shape == (1, rows, 384) and t.equal(y[0], P.puro_gemm_rows(q, s, *codes))
             z = lin(x, lcodes)
             assert t.equal(z[0], P.puro_gemm_rows(*P.puro_fp8_quant_act_1x128(x[0]), *lcodes))
+            assert t.equal(m(x), y)
             if rows % 128:
-                assert t.equal(m(x), y) and t.equal(lin(x), z)
+                assert t.equal(lin(x), z)
+        assert m(whole[:0], codes).shape == (0, 384) and m(whole[:0]).shape == (0, 384)
     with pytest.raises(ValueError):
         lin(whole, lcodes)                                       # codes are not differentiable
+    with pytest.raises(ValueError):
+        m(whole, codes)
+    for wide in (whole.view(128, 512), whole[:, :128].contiguous()):
+        with pytest.raises(ValueError):
+            m(wide)                                              # as many elements do not make it the width
+        with t.no_grad(), pytest.raises(ValueError):
+            m(wide, codes)
     with pytest.raises(P.PuroError):
         m(whole[:100])                                           # a ragged training batch
 
