@@ -98,6 +98,19 @@ def test_range_and_non_finite(P):
     assert float(n) == 10 and (o == 1).all()
 
 
+def test_more_than_32_bits_of_elements(P):
+    t = torch()
+    n = 2 ** 31 + 5
+    g = t.ones(n, dtype=t.bfloat16, device="cuda")
+    norm, _ = P.puro_clip_grad_norm([g[:7].clone(), g], 1024.0)
+    ref = math.sqrt(n + 7)
+    assert abs(float(norm) - ref) <= 2 * U * ref
+    want = float(t.tensor(1024.0 / (ref + 1e-6)).bfloat16())
+    for part in (g[:1000], g[2 ** 30: 2 ** 30 + 1000], g[-1000:]):
+        assert (part == want).all()
+    assert int((g != want).sum()) == 0
+
+
 def test_no_tensors_and_empty_ones(P):
     t = torch()
     assert float(P.puro_grad_norm([])) == 0

@@ -437,3 +437,30 @@ def test_norm_past_32_bit_offsets(P):
     q, s = P.puro_layer_norm_quant(x, w, b)
     q2, s2 = P.puro_layer_norm_quant(v, w, b)
     assert t.equal(q, q2) and t.equal(s, s2)
+
+
+def test_norm_past_32_bit_elements(P):
+    """More than 2^31 elements: the last rows, and the last token block of every column, as by themselves."""
+    t = torch()
+    T, C = 262272, 8192
+    assert T * C > 2 ** 31
+    g = t.Generator(device="cuda")
+    g.manual_seed(1)
+    x = t.randn((T, C), generator=g, device="cuda", dtype=t.bfloat16)
+    w, b = t.randn(C, device="cuda"), t.randn(C, device="cuda")
+    tail = slice(T - 128, T)
+    say(f"[norm, large] {T}x{C}")
+    y, m, r = P.puro_layer_norm(x, w, b)
+    y1, m1, r1 = P.puro_layer_norm(x[tail], w, b)
+    assert t.equal(y[tail], y1) and t.equal(m[tail], m1) and t.equal(r[tail], r1)
+    dx, dw, db = P.puro_layer_norm_backward(y, x, w, m, r)
+    dx1, _, _ = P.puro_layer_norm_backward(y1, x[tail], w, m1, r1)
+    assert t.equal(dx[tail], dx1) and dw.isfinite().all() and db.isfinite().all()
+    del dx, y
+    q, s, qT, sT, _, _ = P.puro_layer_norm_quant_dual(x, w, b)
+    q1, s1, qT1, sT1, _, _ = P.puro_layer_norm_quant_dual(x[tail], w, b)
+    assert t.equal(q[tail], q1) and t.equal(s[:, tail], s1)
+    assert t.equal(qT[:, tail], qT1) and t.equal(sT[-1:], sT1)
+    del q, qT
+    q, s = P.puro_layer_norm_quant(x, w, b)
+    assert t.equal(q[tail], q1) and t.equal(s[:, tail], s1)
