@@ -83,6 +83,18 @@ bool outputs_overlap(const std::vector<puro::GradJob>& jobs) {
   return false;
 }
 
+// Whether [p, p + bytes) shares memory with a tensor of the jobs: such a norm or workspace would be written while
+// other workgroups still read the tensor, or read while they write it.
+bool in_tensors(const std::vector<puro::GradJob>& jobs, const void* p, uintptr_t bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = lo + bytes;
+  for (const puro::GradJob& j : jobs) {
+    const uintptr_t n = (uintptr_t)j.n * (j.bf16 ? 2 : 4);
+    const uintptr_t s = reinterpret_cast<uintptr_t>(j.src), d = reinterpret_cast<uintptr_t>(j.dst);
+    if ((lo < s + n && s < hi) || (j.dst && lo < d + n && d < hi)) return true;
+  }
+  return false;
+}
+
 // Checks a job list and translates it (no exception leaves: PURO_ERR_UNSUPPORTED without memory).
 int grad_jobs(const puro_grad_job* jobs, int n_jobs, bool with_dst, std::vector<puro::GradJob>& out) {
   if (n_jobs < 0) return PURO_ERR_SHAPE;
@@ -222,6 +234,8 @@ static int grad_common(const puro_grad_job* jobs, int n_jobs, bool clip, float m
   const int64_t parts = puro::grad_partials(b.data(), n);
   if (parts > 0 && (workspace == nullptr || workspace_bytes < (size_t)parts * sizeof(double))) return PURO_ERR_WORKSPACE;
   if (parts > 0 && !aligned(workspace, 16)) return PURO_ERR_ALIGN;
+  if (clip && in_tensors(b, norm, sizeof(float))) return PURO_ERR_ARG;
+  if (parts > 0 && in_tensors(b, workspace, (uintptr_t)parts * sizeof(double))) return PURO_ERR_ARG;
   double* w = static_cast<double*>(workspace);
   hipError_t e = puro::launch_grad_squares(b.data(), n, w, st);
   if (e != hipSuccess) return from_hip(e);
@@ -246,6 +260,7 @@ int puro_scale_by_norm(const puro_grad_job* jobs, int n_jobs, float max_norm, co
   if (rc != PURO_OK) return rc;
   if (!norm) return PURO_ERR_NULLPTR;
   if (!aligned(norm, 4)) return PURO_ERR_ALIGN;
+  if (in_tensors(b, norm, sizeof(float))) return PURO_ERR_ARG;
   return from_hip(puro::launch_grad_scale(b.data(), (int)b.size(), nullptr, 0, norm, nullptr, max_norm, st));
 }
 

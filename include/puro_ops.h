@@ -104,7 +104,8 @@ typedef struct puro_grad_job {
  * taken and summed in 64 bits, so nothing overflows or is lost below the fp32 range of the result.
  *   jobs : host array (read before the call returns; not kept); any n_jobs >= 0 (0: norm is 0).
  *   norm : fp32 [1], on the device.
- *   workspace : puro_grad_norm_workspace_size(jobs, n_jobs) bytes, 16-byte aligned.
+ *   workspace : puro_grad_norm_workspace_size(jobs, n_jobs) bytes, 16-byte aligned, apart from the tensors
+ *          (else PURO_ERR_ARG).
  */
 int puro_grad_norm(const puro_grad_job* jobs, int n_jobs, float* norm, void* workspace, size_t workspace_bytes,
                    hipStream_t st);
@@ -116,14 +117,15 @@ int puro_grad_norm(const puro_grad_job* jobs, int n_jobs, float* norm, void* wor
  * 1 and dst == src nothing is written.  A norm that is not finite is not hidden: an infinite one gives
  * c = 0 (infinite elements become NaN), a NaN makes every element NaN, as the product says.  A dst
  * that overlaps another job's src or dst, or its own src other than being it, is refused (PURO_ERR_ARG):
- * a gradient that is listed twice is one.
+ * a gradient that is listed twice is one.  So is a norm inside a tensor.
  */
 int puro_clip_grad_norm(const puro_grad_job* jobs, int n_jobs, float max_norm, float* norm, void* workspace,
                         size_t workspace_bytes, hipStream_t st);
 
 /*
  * The second half alone: dst = src * min(1, max_norm / (*norm + 1e-6)) with a norm that is already on
- * the device (fp32 [1]), e.g. one joined over several processes.  Must not overlap any tensor.
+ * the device (fp32 [1]), e.g. one joined over several processes.  It lies outside
+ * the tensors (else PURO_ERR_ARG).
  */
 int puro_scale_by_norm(const puro_grad_job* jobs, int n_jobs, float max_norm, const float* norm, hipStream_t st);
 

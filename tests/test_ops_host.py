@@ -152,6 +152,20 @@ def test_clip_refuses_overlaps():
     assert clip([same, (A16 + 400, A16 + 400, 100, FP32)], ws=None) == WORKSPACE
 
 
+def test_clip_refuses_a_norm_or_workspace_inside_a_tensor():
+    """Both are written while other workgroups read the tensors."""
+    far, ws = A16 + (1 << 20), A16 + (2 << 20)
+    src_dst = (A16, A16 + 4096, 100, FP32)
+    for at in (A16, A16 + 396, A16 + 4096, A16 + 4096 + 396):
+        assert clip([src_dst], norm=at, ws=ws) == ARG
+        assert P.lib.puro_scale_by_norm(jobs(src_dst), 1, 1.0, at, None) == ARG
+    for at in (A16, A16 + 384, A16 + 4096):                             # a workspace of one value, 8 bytes
+        assert clip([src_dst], norm=far, ws=at) == ARG
+    in_place = (A16 + 4, A16 + 4, 100, FP32)                            # the workspace's second half is its first element
+    assert clip([in_place], norm=far, ws=A16) == ARG
+    assert P.lib.puro_grad_norm(jobs((A16 + 4, None, 100, FP32)), 1, far, A16, 1 << 20, None) == ARG
+
+
 def test_grad_workspace_size():
     size = P.lib.puro_grad_norm_workspace_size
     assert size(jobs(), 0) == 0 and size(jobs((A16, None, 0, FP32)), 1) == 0
