@@ -11,8 +11,11 @@
 
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/variable.h>
 
 #include <string>
 #include <vector>
@@ -228,6 +231,13 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+int norm_kind(PyObject* o) {
+  const int64_t kind = as_int(o, "kind");
+  if (kind != PURO_NORM_LAYER && kind != PURO_NORM_RMS)
+    value_error("kind " + std::to_string(kind) + ": expected LAYER_NORM or RMS_NORM");
+  return (int)kind;
+}
+
 // x, weight, bias, eps, kind: what every forward form takes.
 struct NormIn {
   int kind, xd, wd = 0;
@@ -236,9 +246,7 @@ struct NormIn {
   at::ScalarType xt;
   at::Tensor x, weight, bias;
   NormIn(const Call& c, PyObject* const* a) {
-    kind = (int)as_int(a[4], "kind");
-    if (kind != PURO_NORM_LAYER && kind != PURO_NORM_RMS)
-      value_error("kind " + std::to_string(kind) + ": expected LAYER_NORM or RMS_NORM");
+    kind = norm_kind(a[4]);
     eps = (float)as_float(a[3], "eps");
     xd = dtype_code(a[0], "x", xt);
     x = c.rows(a[0], "x", xt, nullptr, ldx);
@@ -322,9 +330,7 @@ PyObject* layer_norm_quant_dual(PyObject* const* a) {
 // dy, x, weight, mean, rstd, kind, dx, dweight, dbias, with_bias, accumulate, workspace
 PyObject* layer_norm_backward(PyObject* const* a) {
   Call c;
-  const int kind = (int)as_int(a[5], "kind");
-  if (kind != PURO_NORM_LAYER && kind != PURO_NORM_RMS)
-    value_error("kind " + std::to_string(kind) + ": expected LAYER_NORM or RMS_NORM");
+  const int kind = norm_kind(a[5]);
   at::ScalarType xt, wt;
   int64_t ldx, lddy, lddx;
   const int xd = dtype_code(a[1], "x", xt);
@@ -453,6 +459,29 @@ PyObject* gemm_rows(PyObject* const* a) {
   return wrap(C);
 }
 
+// leaves: for the forward pass of a step that is being captured into a graph (the current stream records).  A leaf's
+// gradient belongs to the stream that was current when the first graph that reaches it was built, for as long as one of
+// those graphs lives, and the autograd engine joins that stream to the backward pass.  One that does not record breaks
+// the capture from inside the engine, which ends the process: refused here, before the pass starts.
+PyObject* check_capture(PyObject* const* a) {
+  if (!PyTuple_Check(a[0])) type_error("expected a tuple of tensors");
+  for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(a[0]); ++i) {
+    PyObject* o = PyTuple_GET_ITEM(a[0], i);
+    if (!THPVariable_Check(o)) continue;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda() || !t.requires_grad() || !t.is_leaf()) continue;
+    const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
+    if (!node) continue;
+    const auto st = node->stream();
+    const c10::impl::VirtualGuardImpl guard(t.device().type());
+    if (st && *st != guard.getStream(t.device()))
+      throw Refused{PyExc_RuntimeError,
+                    "a step is being captured while the autograd graph of another stream reaches the same parameter or "
+                    "input: delete the outputs of the earlier passes first"};
+  }
+  Py_RETURN_NONE;
+}
+
 // get_device, get_stream, raise_status: called once, before any of the above
 PyObject* init(PyObject* const* a) {
   PyObject** slots[] = {&get_device, &get_stream, &raise_status};
@@ -468,6 +497,7 @@ PyObject* init(PyObject* const* a) {
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<n, name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     PURO_ENTRY(init, 3),
+    PURO_ENTRY(check_capture, 1),
     PURO_ENTRY(layer_norm, 9),
     PURO_ENTRY(layer_norm_quant, 9),
     PURO_ENTRY(layer_norm_quant_dual, 11),

@@ -25,6 +25,7 @@ from torch.autograd.function import once_differentiable
 from . import (DGRAD, FWD, LAYER_NORM, OUT_BF16, OUT_FP32, RMS_NORM, WGRAD, puro_fp8_gemm, puro_fp8_gemm_accumulate,
                puro_fp8_quant_act_dual, puro_fp8_quant_w_128x128, puro_gemm_rows, puro_layer_norm,
                puro_layer_norm_backward, puro_layer_norm_quant, puro_layer_norm_quant_dual)
+from ._marshal import check_capture
 from .linear import Fp8Linear, _rows
 
 __all__ = ["Norm", "NormFunction", "Fp8NormLinear", "Fp8NormLinearFunction", "layer_norm", "rms_norm"]
@@ -49,6 +50,12 @@ def _norm_grads(kind, dn, x2, gamma, mean, rstd, weight, bias, need_w, need_b):
     return dx, dw if need_w else None, db if need_b else None
 
 
+def _apply(function, x, *args):
+    if torch.is_grad_enabled() and x.is_cuda and torch.cuda.is_current_stream_capturing():
+        check_capture((x,) + args)
+    return function.apply(x, *args)
+
+
 class NormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps, kind):
@@ -69,12 +76,12 @@ class NormFunction(torch.autograd.Function):
 
 def layer_norm(x, weight, bias=None, eps: float = 1e-5):
     """Layer norm over the last dimension of x (differentiable)."""
-    return NormFunction.apply(x, weight, bias, eps, LAYER_NORM)
+    return _apply(NormFunction, x, weight, bias, eps, LAYER_NORM)
 
 
 def rms_norm(x, weight, eps: float = 1e-6):
     """RMS norm over the last dimension of x (differentiable)."""
-    return NormFunction.apply(x, weight, None, eps, RMS_NORM)
+    return _apply(NormFunction, x, weight, None, eps, RMS_NORM)
 
 
 class Norm(torch.nn.Module):
@@ -92,7 +99,7 @@ class Norm(torch.nn.Module):
             p.main_grad = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
 
     def forward(self, x):
-        return NormFunction.apply(x, self.weight, self.bias, self.eps, self.kind)
+        return _apply(NormFunction, x, self.weight, self.bias, self.eps, self.kind)
 
     def extra_repr(self) -> str:
         return f"{self.features}, kind={'layer' if self.kind == LAYER_NORM else 'rms'}, eps={self.eps}"
@@ -158,7 +165,7 @@ class Fp8NormLinear(torch.nn.Module):
         if torch.is_grad_enabled():
             if codes is not None:
                 raise ValueError("codes: a weight quantized beforehand is for use without gradients (torch.no_grad)")
-            return Fp8NormLinearFunction.apply(x, n.weight, n.bias, w, n.eps, n.kind)
+            return _apply(Fp8NormLinearFunction, x, n.weight, n.bias, w, n.eps, n.kind)
         wq, ws = self.quantize_weight() if codes is None else codes
         xq, xs = puro_layer_norm_quant(_rows(x, w.shape[1]), n.weight, n.bias, eps=n.eps, kind=n.kind)
         return puro_gemm_rows(xq, xs, wq, ws).view(*x.shape[:-1], w.shape[0])

@@ -197,3 +197,68 @@ def test_step_with_clipping(P):
     for g, o in zip(grads, before):
         assert (g.double() - o.double() * (0.25 / (ref + 1e-6))).abs().max() <= 6 * 2.0 ** -24 * g.abs().max().double()
     assert abs(float(P.puro_grad_norm(grads)) - 0.25) < 1e-6
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+def test_step_in_a_graph(P, kind):
+    """Forward, backward and clipping captured together; every replay against an eager step on other inputs."""
+    import copy
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.clip import clip_grad_norm_
+    m = layer(P, kind)
+    m.enable_main_grad()
+    e = copy.deepcopy(m)
+    e.enable_main_grad()
+    xin = t.randn((128, 256), device="cuda").bfloat16().requires_grad_(True)
+    dyin = t.randn((128, 384), device="cuda").bfloat16()
+
+    def step(mod, x, dy):
+        for p in mod.parameters():
+            p.main_grad.zero_()
+        y = mod(x)
+        y.backward(dy)
+        return y.detach(), clip_grad_norm_(mod.parameters(), 0.5)
+
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        step(m, xin, dyin)
+    t.cuda.current_stream().wait_stream(side)
+    xin.grad = None
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        y, norm = step(m, xin, dyin)
+    x0, dy0 = xin.detach().clone(), dyin.clone()
+    for k in range(3):
+        with t.no_grad():
+            xin.copy_(x0 * (k + 1) - k)
+            dyin.copy_(dy0 / (k + 1))
+        graph.replay()
+        t.cuda.synchronize()
+        x = xin.detach().clone().requires_grad_(True)
+        ey, enorm = step(e, x, dyin)
+        assert t.equal(y, ey) and t.equal(norm, enorm) and t.equal(xin.grad, x.grad), k
+        for a, b in zip(m.parameters(), e.parameters()):
+            assert a.main_grad.any() and t.equal(a.main_grad, b.main_grad), k
+
+
+def test_capture_over_a_living_graph_is_refused(P):
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.norm import Norm
+    m, n = layer(P, 1), Norm(256, 0, device="cuda")
+    x = t.randn((128, 256), device="cuda").bfloat16()
+    living = [m(x), n(x)]
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        out = x * 2
+        for mod in (m, n):
+            with pytest.raises(RuntimeError, match="captured"):
+                mod(x)
+        with t.no_grad():
+            y = n(x)                                             # without gradients there is nothing to join
+    graph.replay()
+    t.cuda.synchronize()
+    assert t.equal(out, x * 2) and t.equal(y, n(x).detach())
+    for z in living:
+        z.backward(t.ones_like(z))                               # the eager graphs are as they were
+    assert n.weight.grad.isfinite().all() and m.linear.weight.grad.isfinite().all()
