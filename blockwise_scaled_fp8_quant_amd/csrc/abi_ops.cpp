@@ -284,8 +284,8 @@ int puro_gemm_rows(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t ld
     if (!aligned(A, 16) || !aligned(B, 16) || !aligned(sA, 4) || !aligned(sB, 4)) return PURO_ERR_ALIGN;
     if (lda < K || ldb < K || lda % 16 || ldb % 16) return PURO_ERR_LD;
   }
-  // (the column index of a workgroup's last strips may pass N by three strips, in 32 bits)
-  if (M > kIntMax || N > kIntMax / 2 || K > kIntMax) return PURO_ERR_UNSUPPORTED;
+  // (a launch counts its threads, 8 to a column, in 32 bits)
+  if (M > kIntMax || N > kIntMax / 4 || K > kIntMax) return PURO_ERR_UNSUPPORTED;
   if (K > 0 && (lda > kMaxGemmLd || ldb > kMaxGemmLd)) return PURO_ERR_UNSUPPORTED;
   const size_t need = out_dtype == PURO_OUT_BF16 ? puro_gemm_rows_workspace_size(M, N, K) : 0;
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PURO_ERR_WORKSPACE;

@@ -21,6 +21,8 @@
 // bf16 too.  The conversion costs 4 to 9% up to 64 rows and 10 to 30% at 200, where matrix work shows.
 // The weight is the first operand: a lane then holds four consecutive columns of one output row, and
 // its row scale is one value.
+#include <algorithm>
+
 #include "codec.hpp"
 #include "gemm_args.hpp"
 #include "internal.hpp"
@@ -210,7 +212,6 @@ __global__ __launch_bounds__(64 * WK) void gemm_rows_kernel(RowsArgs p) {
 template <int MT, int NT, int WK>
 hipError_t go(const RowsArgs& a, bool out_bf16, hipStream_t st) {
   const dim3 grid((unsigned)((a.N + 16 * NT - 1) / (16 * NT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
-  if (grid.y > 65535u) return hipErrorInvalidConfiguration;   // over 4 million fp32 rows
   if (out_bf16)
     hipLaunchKernelGGL((gemm_rows_kernel<MT, NT, WK, true>), grid, dim3(64 * WK), 0, st, a);
   else
@@ -255,13 +256,19 @@ hipError_t launch_gemm_rows(int64_t M, int64_t N, int64_t K, const uint8_t* A, i
                                      workspace, workspace_bytes, st, M);
     if (e != hipSuccess || lead == M) return e;
   }
-  const int64_t rows = M - lead;
-  const RowsArgs a = {(int)rows, (int)N, (int)K, A + lead * lda, lda, sA + lead, M, B, ldb, sB,
-                      static_cast<uint8_t*>(C) + lead * ldc * (out_bf16 ? 2 : 4), ldc};
-  if (rows <= 16) return by_strips<1>(a, out_bf16, st);
-  if (rows <= 32) return by_strips<2>(a, out_bf16, st);
-  if (rows <= 48) return by_strips<3>(a, out_bf16, st);   // (37 x 4096 x 2048: 4.9 us, 5.4 as 64 rows)
-  return by_strips<4>(a, out_bf16, st);
+  constexpr int64_t kMost = 65535 * 64;   // rows that a launch's second dimension holds (fp32 outputs may have more)
+  for (int64_t m = lead; m < M; m += kMost) {
+    const int64_t rows = std::min(M - m, kMost);
+    const RowsArgs a = {(int)rows, (int)N, (int)K, A + m * lda, lda, sA + m, M, B, ldb, sB,
+                        static_cast<uint8_t*>(C) + m * ldc * (out_bf16 ? 2 : 4), ldc};
+    hipError_t e;
+    if (rows <= 16) e = by_strips<1>(a, out_bf16, st);
+    else if (rows <= 32) e = by_strips<2>(a, out_bf16, st);
+    else if (rows <= 48) e = by_strips<3>(a, out_bf16, st);   // (37 x 4096 x 2048: 4.9 us, 5.4 as 64 rows)
+    else e = by_strips<4>(a, out_bf16, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace puro

@@ -638,10 +638,13 @@ hipError_t launch_fwd(NormArgs a, hipStream_t st) {
     // the row-wise arrays; one row where the input would not give the card 2048 waves otherwise.  (8 rows leave
     // too few workgroups to share evenly: 16384 x 1024 bf16 15.3 us, 12.2 with 4; 3000 x 3000 10.2 and 9.2; 16384 x 2048
     // 23.5 and 23.2.  2 rows: 36.0 us at 16384 x 2047, 32.4 with 4.)
-    const int64_t r = std::max<int64_t>(1, std::min<int64_t>(4, a.T / (131072 / lpr)));
+    int64_t r = std::max<int64_t>(1, std::min<int64_t>(4, a.T / (131072 / lpr)));
+    // (a launch counts its threads in 32 bits: past 2^30 of the shortest rows a team takes more)
+    const int64_t most = 0xFFFFFFFFll / threads * teams;
+    r = std::max(r, (a.T + most - 1) / most);
+    if (r > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
     a.rows_per_team = (int)r;
     const int64_t blocks = (a.T + teams * r - 1) / (teams * r);
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), 0, st, a);
     return hipGetLastError();
   };

@@ -137,7 +137,7 @@ size_t puro_grad_norm_workspace_size(const puro_grad_job* jobs, int n_jobs);
  *   A : uint8 codes [M, K], row stride lda; sA: fp32 [K/128][M]     (puro_fp8_quant_act_1x128)
  *   B : uint8 codes [N, K], row stride ldb; sB: fp32 [N/128][K/128] (puro_fp8_quant_w_128x128)
  *   C : [M, N] of out_dtype, row stride ldc.  N % 128 == 0, K % 128 == 0.  K == 0 gives zeros.
- *         lda, ldb <= 2^29 (else PURO_ERR_UNSUPPORTED).
+ *         M, K < 2^31, N < 2^29, lda, ldb <= 2^29 (else PURO_ERR_UNSUPPORTED).
  *   workspace : puro_gemm_rows_workspace_size(M, N, K) bytes, 16-byte aligned (NULL when 0); an fp32 output needs
  *         none.
  * Alignment as puro_fp8_gemm (16-byte pointers and row strides; sA and sB 4-byte).  Codes are decoded exactly to bf16 and

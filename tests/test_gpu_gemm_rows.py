@@ -200,3 +200,17 @@ def test_weights_past_32_bit_offsets(P):
     out = big[: 128 * ld // 32 * 32].view(t.bfloat16).as_strided((2, 128), ((1 << 31) + 64, 1), 0)
     P.puro_gemm_rows(A, sA, B, sB, C=out)
     assert t.equal(out, P.puro_gemm_rows(A, sA, B, sB))
+
+
+def test_more_fp32_rows_than_a_launch_holds(P):
+    """The rows on both sides of the limit and the last ones, as by themselves (one slice: any split sums alike)."""
+    t = torch()
+    M = 65535 * 64 + 3
+    A, sA, B, sB = operands(64, 128, 128, 9)
+    reps = M // 64 + 1
+    A, sA = A.repeat(reps, 1)[:M], sA.repeat(1, reps)[:, :M].contiguous()
+    say(f"[rows, large] {M}x128x128 fp32")
+    C = P.puro_gemm_rows(A, sA, B, sB, out_dtype=P.OUT_FP32)
+    ref = P.puro_gemm_rows(A[:64], sA[:, :64].contiguous(), B, sB, out_dtype=P.OUT_FP32)
+    assert ref.any() and t.equal(C[:M // 64 * 64].view(-1, 64, 128), ref.expand(M // 64, 64, 128))
+    assert t.equal(C[-3:], ref[:3])

@@ -464,3 +464,19 @@ def test_norm_past_32_bit_elements(P):
     del q, qT
     q, s = P.puro_layer_norm_quant(x, w, b)
     assert t.equal(q[tail], q1) and t.equal(s[:, tail], s1)
+
+
+def test_more_short_rows_than_a_launch_has_threads(P):
+    """2^30 rows and some: an RMS norm of single elements is their sign, but for eps (0: exactly one rounding of |x|'s
+    reciprocal root, 2^-8 in bf16); the rows at the end as by themselves."""
+    t = torch()
+    T = (1 << 30) + 77
+    x = t.ones((T, 1), device="cuda", dtype=t.bfloat16)
+    x[::3] = -2
+    w = t.ones(1, device="cuda", dtype=t.bfloat16)
+    say(f"[norm, long] {T}x1")
+    y, _, r = P.puro_layer_norm(x, w, eps=0.0, kind=P.RMS_NORM)
+    assert float((y.abs() - 1).abs().max()) <= 2.0 ** -8 and t.equal(y < 0, x < 0)
+    tail = x[-1000:].contiguous()
+    y1, _, r1 = P.puro_layer_norm(tail, w, eps=0.0, kind=P.RMS_NORM)
+    assert t.equal(y[-1000:], y1) and t.equal(r[-1000:], r1)

@@ -152,6 +152,12 @@ def test_clip_refuses_overlaps():
     assert clip([same, (A16 + 400, A16 + 400, 100, FP32)], ws=None) == WORKSPACE
 
 
+def test_rows_refuses_more_columns_than_a_launch_holds():
+    """Eight threads to a column, counted in 32 bits."""
+    N = 1 << 29
+    assert rows(N=N, ldc=N) == UNSUP and rows(N=N - 128, ldc=N, M=1 << 31) == UNSUP
+
+
 def test_clip_refuses_a_norm_or_workspace_inside_a_tensor():
     """Both are written while other workgroups read the tensors."""
     far, ws = A16 + (1 << 20), A16 + (2 << 20)
