@@ -5,20 +5,23 @@
 //
 // With few rows the product is bound by reading the weight codes once (N K bytes), and a CU takes at most about
 // 25 bytes per ns of them from HBM (measured: 256 CUs stream 6.4 TB/s), so every CU has to have its share.  A workgroup owns
-// NT strips of 16 columns for 16 MT rows, with NT chosen so that about one workgroup per CU is left (launch_gemm_rows),
-// and splits the contraction over its waves, a run of 128-deep slices each: it has as many weight lines in flight as
-// it has waves, without a second launch to join the parts.  The waves' fp32 sums are joined through LDS in order.
+// NT strips of 16 columns for 16 MT rows, chosen by what a CU then loads (by_tile), and splits the contraction over its
+// waves, a run of 128-deep slices each: it has as many weight lines in flight as it has waves, without a second launch
+// to join the parts.  The waves' fp32 sums are joined through LDS in order.
 //
-// A slice of a 16-row fragment is two 16-byte loads per lane, eight lanes to a row's 128-byte line, and is
-// turned into the matrix instruction's order (lane l: row l % 16, 16-byte chunks l / 16 and l / 16 + 4) through
-// the wave's own piece of LDS.  Loading that order directly costs 77 cycles per load instruction (each lane a request of its
-// own) against 16; 64 rows x 6144 deep x 2048 columns took 17.4 us so and take 12.2.  Chunk c of row r is kept
-// at c ^ (r / 2 % 8), which spreads a read's 16 rows over all banks.  Both operands use the same order of
-// the contraction, so the order itself does not matter.
+// A slice of a 16-row fragment is two 16-byte loads per lane, eight lanes to a row's 128-byte line, that go straight into
+// the wave's own piece of LDS, and is read from there in the matrix instruction's order (lane l: row l % 16, 16-byte
+// chunks l / 16 and l / 16 + 4).  Loading that order directly costs 77 cycles per load instruction (each lane a request of
+// its own) against 16.  Chunk c of row r is kept in slot c ^ (r / 2 % 8), which spreads a read's 16 rows over all
+// banks; a load fills the slots in order, so the lanes take their row's chunks in that order.  Both operands use the same
+// order of the contraction, so the order itself does not matter.
+// The next slice is on its way as soon as this one has left LDS for registers.  Loads through registers left none
+// for a slice ahead beyond 32 rows and 3 strips (200 x 6144 deep x 2048, same tile: 14.3 us so, 12.9 as it is).
 //
 // The codes are converted, exactly, to bf16, whose matrix instruction keeps a full fp32 sum (1e-7 off, relative); the
 // FP8 one's sum of 128 products is about 1.4e-5 off, which an fp32 output shows and a sum that cancels shows in
-// bf16 too.  The conversion costs 4 to 9% up to 64 rows and 10 to 30% at 200, where matrix work shows.
+// bf16 too.  The conversion costs 2 to 9% up to 64 rows and 6 to 11% at 200, where matrix work shows.  (Its
+// 16 x 16 x 32 form is 9e-5 off.)
 // The weight is the first operand: a lane then holds four consecutive columns of one output row, and
 // its row scale is one value.
 #include <algorithm>
@@ -62,12 +65,6 @@ struct Frag {
   u32x4 w[2];
 };
 
-// Keeps the compiler from moving one lane's LDS reads over another's writes; the hardware does a wave's in order.
-__device__ __forceinline__ void wave_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // A fragment as the matrix instruction takes it, in four parts of the slice.
 struct Operand {
   bf16x8_t v[4];
@@ -83,23 +80,25 @@ __global__ __launch_bounds__(64 * WK) void gemm_rows_kernel(RowsArgs p) {
   constexpr int kJoin = WK * kTiles * 64 * 16, kStages = WK * kStage;
   __shared__ __attribute__((aligned(16))) uint8_t smem[kJoin > kStages ? kJoin : kStages];
   f32x4_t (*join)[kTiles][64] = reinterpret_cast<f32x4_t (*)[kTiles][64]>(smem);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int n0 = blockIdx.x * 16 * NT;
   const int m0 = blockIdx.y * 16 * MT;
   const int nk = p.K >> 7;
   uint8_t* stage = smem + wave * kStage;
 
-  // loads: lane l takes 16 bytes of row l / 8 (and l / 8 + 8)
+  // loads: lane l fills slot l % 8 of row l / 8 (and of row l / 8 + 8)
   const int lr = lane >> 3, lc = lane & 7;
-  const uint8_t* bp[NT];
+  const int c0 = 16 * (lc ^ (lr >> 1)), c1 = c0 ^ 64;
+  const uint8_t* bp[NT][2];
   const float* sb[NT];
   const uint8_t* ap[MT][2];
   int mrow[MT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int n = n0 + 16 * j < p.N ? n0 + 16 * j : p.N - 16;   // strips past N repeat the last one, likewise
-    bp[j] = p.B + (int64_t)(n + lr) * p.ldb + 16 * lc;
+    bp[j][0] = p.B + (int64_t)(n + lr) * p.ldb + c0;
+    bp[j][1] = p.B + (int64_t)(n + lr + 8) * p.ldb + c1;
     sb[j] = p.sB + (int64_t)(n >> 7) * nk;
   }
 #pragma unroll
@@ -109,11 +108,9 @@ __global__ __launch_bounds__(64 * WK) void gemm_rows_kernel(RowsArgs p) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int mm = m0 + 16 * i + 8 * h + lr;
-      ap[i][h] = p.A + (int64_t)(mm < p.M ? mm : p.M - 1) * p.lda + 16 * lc;
+      ap[i][h] = p.A + (int64_t)(mm < p.M ? mm : p.M - 1) * p.lda + (h ? c1 : c0);
     }
   }
-  uint8_t* wr0 = stage + lr * 128 + ((lc ^ ((lr >> 1) & 7)) * 16);
-  uint8_t* wr1 = stage + (lr + 8) * 128 + ((lc ^ (((lr + 8) >> 1) & 7)) * 16);
   const uint8_t* rd0 = stage + l16 * 128 + ((g ^ ((l16 >> 1) & 7)) * 16);
   const uint8_t* rd1 = stage + l16 * 128 + (((g + 4) ^ ((l16 >> 1) & 7)) * 16);
 
@@ -124,45 +121,36 @@ __global__ __launch_bounds__(64 * WK) void gemm_rows_kernel(RowsArgs p) {
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   const int per = (nk + WK - 1) / WK, kbeg = wave * per, kend = kbeg + per < nk ? kbeg + per : nk;
-  // Up to 32 rows and 3 strips the next slice is loaded as soon as this one is in LDS (1 x 6144 deep x 2048: 6.2 us, 7.4
-  // without).  Larger tiles lack the registers: 64 x 2048 deep x 4096 takes 9.8 us so and 5.7 as it is, one row with 4 strips
-  // (151936 columns) 69.7 and 59.1.
-  constexpr bool kAhead = MT <= 2 && NT <= 3;
-  u32x4 bl[NT][2], al[MT][2];
   float sa[MT];
   auto fetch = [&](int kb) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      bl[j][0] = *reinterpret_cast<const u32x4*>(bp[j] + (int64_t)kb * 128);
-      bl[j][1] = *reinterpret_cast<const u32x4*>(bp[j] + 8 * p.ldb + (int64_t)kb * 128);
-    }
+    for (int f = 0; f < NT + MT; ++f)
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* src = (f < NT ? bp[f < NT ? f : 0][h] : ap[f < NT ? 0 : f - NT][h]) + (int64_t)kb * 128;
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                         (__attribute__((address_space(3))) void*)(stage + f * 2048 + h * 1024), 16, 0, 0);
+      }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) al[i][h] = *reinterpret_cast<const u32x4*>(ap[i][h] + (int64_t)kb * 128);
-      sa[i] = p.sA[(int64_t)kb * p.lds + mrow[i]];
-    }
+    for (int i = 0; i < MT; ++i) sa[i] = p.sA[(int64_t)kb * p.lds + mrow[i]];
   };
-  if (kAhead && kbeg < kend) fetch(kbeg);
+  if (kbeg < kend) fetch(kbeg);
   for (int kb = kbeg; kb < kend; ++kb) {
-    if (!kAhead) fetch(kb);
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      *reinterpret_cast<u32x4*>(wr0 + j * 2048) = bl[j][0];
-      *reinterpret_cast<u32x4*>(wr1 + j * 2048) = bl[j][1];
-    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the slice is in LDS
+    __builtin_amdgcn_sched_barrier(0);
+    Frag raw[NT + MT];
     float sc[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      *reinterpret_cast<u32x4*>(wr0 + (NT + i) * 2048) = al[i][0];
-      *reinterpret_cast<u32x4*>(wr1 + (NT + i) * 2048) = al[i][1];
-      sc[i] = sa[i];
+    for (int f = 0; f < NT + MT; ++f) {
+      raw[f].w[0] = *reinterpret_cast<const u32x4*>(rd0 + f * 2048);
+      raw[f].w[1] = *reinterpret_cast<const u32x4*>(rd1 + f * 2048);
     }
-    if (kAhead && kb + 1 < kend) fetch(kb + 1);
-    wave_order();   // the LDS piece is the wave's own: its instructions reach it in order
-    auto fragment = [&](int f) {
-      return Operand(Frag{*reinterpret_cast<const u32x4*>(rd0 + f * 2048), *reinterpret_cast<const u32x4*>(rd1 + f * 2048)});
-    };
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sc[i] = sa[i];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // and read: the next one may overwrite it
+    __builtin_amdgcn_sched_barrier(0);
+    if (kb + 1 < kend) fetch(kb + 1);
+    auto fragment = [&](int f) { return Operand(raw[f]); };
     bf16x8_t bv[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -183,7 +171,6 @@ __global__ __launch_bounds__(64 * WK) void gemm_rows_kernel(RowsArgs p) {
         for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(v[r], s, acc[i][j][r]);
       }
     }
-    wave_order();
   }
   __syncthreads();
 
@@ -219,22 +206,62 @@ hipError_t go(const RowsArgs& a, bool out_bf16, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Strips per workgroup: the fewest that leave at most one workgroup per CU (256).  Fewer would give some CUs two and others one
-// (N = 12288, M <= 16: 7.0 us with 3 strips, 8.6 with 1), more would leave CUs idle (N = 4096: 4.1 us with 1,
-// 4.5 with 2).  A lone strip gets 16 waves (K = 6144: 6.5 us, 7.2 with 8).
+// Waves of a workgroup, all on the same tile.  A lone strip has 16 where each gets more than one slice (1 x 6144 deep x
+// 2048: 6.4 us, 7.0 with 8; 1 x 2048 deep x 4096: 4.05 us with 16, 3.86 with 8).  Where the card is filled more than
+// once and a CU's LDS holds one workgroup of 8, two of 4 work while the other starts or ends (256 x 2048 deep x
+// 12288: 24.0 us, 27.3 with 8); a single round has 8 (200 x 6144 deep x 2048: 13.7 us, 18.1 with 4).
+template <int MT, int NT>
+hipError_t by_waves(const RowsArgs& a, bool out_bf16, hipStream_t st, int64_t workgroups) {
+  if constexpr (NT == 1) {
+    if (a.K > 16 * 128) return go<MT, NT, 16>(a, out_bf16, st);
+  }
+  if constexpr (NT > 2 && MT + NT > 5) {
+    if (workgroups > 256) return go<MT, NT, 4>(a, out_bf16, st);
+  }
+  return go<MT, NT, 8>(a, out_bf16, st);
+}
+
+// The tile: the one with which a CU loads least, rounds of 256 workgroups times MT + NT fragments a slice; among equals the
+// one with most workgroups, then fewest rows.  (64 x 6144 deep x 2048: 8.4 us as 16 x 32 tiles, 12.4 as 64 x 16, which
+// leave half the CUs idle; 64 x 2048 deep x 4096: 4.9 as 32 x 32, 6.3 as 64 x 16; 37 x 2048 deep x 12288: 9.2 as
+// 48 x 48, which makes 256 workgroups.)
 template <int MT>
-hipError_t by_strips(const RowsArgs& a, bool out_bf16, hipStream_t st) {
-  const int64_t strips = a.N / 16, row_blocks = (a.M + 16 * MT - 1) / (16 * MT);
-  auto fits = [&](int64_t nt) { return (strips + nt - 1) / nt * row_blocks <= 256; };
-  if (fits(1)) return go<MT, 1, 16>(a, out_bf16, st);
-  if (fits(2)) return go<MT, 2, 8>(a, out_bf16, st);
-  if (fits(3)) return go<MT, 3, 8>(a, out_bf16, st);
-  return go<MT, 4, 8>(a, out_bf16, st);
+hipError_t by_strips(const RowsArgs& a, bool out_bf16, hipStream_t st, int nt, int64_t workgroups) {
+  if constexpr (MT < 4) {   // (4 x 1 never is that: 2 x 2 covers as much)
+    if (nt == 1) return by_waves<MT, 1>(a, out_bf16, st, workgroups);
+  }
+  if (nt == 2) return by_waves<MT, 2>(a, out_bf16, st, workgroups);
+  if (nt == 3) return by_waves<MT, 3>(a, out_bf16, st, workgroups);
+  return by_waves<MT, 4>(a, out_bf16, st, workgroups);
+}
+
+hipError_t by_tile(const RowsArgs& a, bool out_bf16, hipStream_t st) {
+  const uint32_t M = (uint32_t)a.M, strips = (uint32_t)a.N / 16;
+  const int64_t row_blocks[4] = {(M + 15) / 16, (M + 31) / 32, (M + 47) / 48, (M + 63) / 64};
+  const int64_t col_blocks[4] = {strips, (strips + 1) / 2, (strips + 2) / 3, (strips + 3) / 4};
+  int mt = 4, nt = 4;
+  int64_t best = INT64_MAX, workgroups = 0;
+  for (int m = 1; m <= 4; ++m) {
+    if (row_blocks[m - 1] > 65535) continue;   // the launch's second dimension
+    for (int n = m < 4 ? 1 : 2; n <= 4; ++n) {
+      const int64_t w = row_blocks[m - 1] * col_blocks[n - 1], cost = (w + 255) / 256 * (m + n);
+      if (cost < best || (cost == best && w > workgroups)) {
+        best = cost;
+        workgroups = w;
+        mt = m;
+        nt = n;
+      }
+    }
+  }
+  if (mt == 1) return by_strips<1>(a, out_bf16, st, nt, workgroups);
+  if (mt == 2) return by_strips<2>(a, out_bf16, st, nt, workgroups);
+  if (mt == 3) return by_strips<3>(a, out_bf16, st, nt, workgroups);
+  return by_strips<4>(a, out_bf16, st, nt, workgroups);
 }
 
 // Leading rows (a multiple of 128) that go through the 256 x 256 tiles of the blockwise GEMM: all there are, where their
-// product is long enough to fill it.  Both sides, us: 512 x 12288 x 2048 51 here, 26 there; 1024 x 4096 x 2048 32 and
-// 27; 256 x 12288 x 2048 28 and 27; 512 x 2048 x 6144 22 and 30; 2048 x 1024 x 1024 12 and 15.
+// product is long enough to fill it.  Both sides, us: 512 x 12288 x 2048 42 here, 26 there; 1024 x 4096 x 2048 28 and
+// 27; 256 x 12288 x 2048 24 and 27; 512 x 2048 x 6144 22 and 30; 2048 x 1024 x 1024 10 and 15.
 int64_t leading_rows(int64_t M, int64_t N, int64_t K) {
   const int64_t rows = M - M % 128;
   return (double)rows * (double)N * (double)K >= (double)(int64_t(1) << 33) ? rows : 0;
@@ -261,11 +288,7 @@ hipError_t launch_gemm_rows(int64_t M, int64_t N, int64_t K, const uint8_t* A, i
     const int64_t rows = std::min(M - m, kMost);
     const RowsArgs a = {(int)rows, (int)N, (int)K, A + m * lda, lda, sA + m, M, B, ldb, sB,
                         static_cast<uint8_t*>(C) + m * ldc * (out_bf16 ? 2 : 4), ldc};
-    hipError_t e;
-    if (rows <= 16) e = by_strips<1>(a, out_bf16, st);
-    else if (rows <= 32) e = by_strips<2>(a, out_bf16, st);
-    else if (rows <= 48) e = by_strips<3>(a, out_bf16, st);   // (37 x 4096 x 2048: 4.9 us, 5.4 as 64 rows)
-    else e = by_strips<4>(a, out_bf16, st);
+    const hipError_t e = by_tile(a, out_bf16, st);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

@@ -214,3 +214,18 @@ def test_more_fp32_rows_than_a_launch_holds(P):
     ref = P.puro_gemm_rows(A[:64], sA[:, :64].contiguous(), B, sB, out_dtype=P.OUT_FP32)
     assert ref.any() and t.equal(C[:M // 64 * 64].view(-1, 64, 128), ref.expand(M // 64, 64, 128))
     assert t.equal(C[-3:], ref[:3])
+
+
+# one shape for each tile and split over waves of the kernel, most with columns and rows left over
+@pytest.mark.parametrize("M,N", [(1, 128), (1, 4224), (1, 8320), (1, 16512), (3, 12416), (5, 24704), (34, 1408), (19, 6272),
+                                 (19, 8320), (19, 16512), (19, 12416), (19, 24704), (67, 1664), (34, 6272), (34, 8320),
+                                 (34, 16512), (34, 12416), (34, 24704), (145, 2560), (49, 8320), (49, 16512), (49, 12416),
+                                 (49, 24704), (300, 12416)])
+def test_every_tile(P, M, N):
+    """A contraction that leaves some waves a slice less, and some none."""
+    t = torch()
+    for K in (384, 1152, 2432):
+        A, sA, B, sB = operands(M, N, K, M + N)
+        say(f"[rows] M,N,K={M},{N},{K}")
+        check(P, A, sA, B, sB, P.puro_gemm_rows(A, sA, B, sB, out_dtype=P.OUT_FP32), t.float32, (M, N, K))
+        check(P, A, sA, B, sB, P.puro_gemm_rows(A, sA, B, sB), t.bfloat16, (M, N, K))
