@@ -35,6 +35,13 @@ struct Raw8 {
   u32x4 w[BF16 ? 1 : 2];
 };
 
+// Makes the compiler take a value for new, so that what it computed from it before does not stay in registers.
+template <bool BF16>
+__device__ __forceinline__ void forget(Raw8<BF16>& r) {
+  asm volatile("" : "+v"(r.w[0]));
+  if constexpr (!BF16) asm volatile("" : "+v"(r.w[1]));
+}
+
 // memory vectors of element alignment
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
@@ -505,28 +512,37 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, in
     nmean = ok && a.layer ? a.mean[r] : 0.f;
     nrstd = ok ? a.rstd[r] : 0.f;
   };
-  fetch(row);
+  // The widest class has no registers for a row ahead nor for a row's differences between their two uses: it keeps the row
+  // as loaded and takes them again (2000 x 16384: bf16 65 us, fp32 110; 88 and 201 as the others do it, spilling).
+  constexpr bool kAhead = ITER < 4;
+  if (kAhead) fetch(row);
   for (int k = 0; k < rows_per_team; ++k, row += stride) {
+    if (!kAhead) fetch(row);
     const bool ok = row < a.T;
     const float mean = nmean, rstd = nrstd;
-    float xh[ITER][8], d[ITER][8];
+    float xh[kAhead ? ITER : 1][8], d[kAhead ? ITER : 1][8];
     float s1 = 0.f, s2 = 0.f;
+    auto take = [&](int i, float (&x)[8], float (&v)[8]) {
+      unpack8<BF16, VEC>(nx[i], nv[i], x);
+      unpack8<BF16, VEC>(ny[i], nv[i], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = (x[j] - mean) * rstd;
+    };
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-      unpack8<BF16, VEC>(nx[i], nv[i], xh[i]);
-      unpack8<BF16, VEC>(ny[i], nv[i], d[i]);
+      float (&x)[8] = xh[kAhead ? i : 0], (&v)[8] = d[kAhead ? i : 0];
+      take(i, x, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // a column that does not exist has dy = 0 and weight 0: it adds nothing to any sum
-        xh[i][j] = (xh[i][j] - mean) * rstd;
-        dg[i][j] = __builtin_fmaf(d[i][j], xh[i][j], dg[i][j]);
-        db[i][j] += d[i][j];
-        d[i][j] *= g[i][j];
-        s1 += d[i][j];
-        s2 = __builtin_fmaf(d[i][j], xh[i][j], s2);
+        dg[i][j] = __builtin_fmaf(v[j], x[j], dg[i][j]);
+        db[i][j] += v[j];
+        v[j] *= g[i][j];
+        s1 += v[j];
+        s2 = __builtin_fmaf(v[j], x[j], s2);
       }
     }
-    if (k + 1 < rows_per_team) fetch(row + stride);
+    if (kAhead && k + 1 < rows_per_team) fetch(row + stride);
     s1 = lanes_sum<LPR>(s1);
     s2 = lanes_sum<LPR>(s2);
     if constexpr (LPR > 64) {
@@ -549,8 +565,16 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, in
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
       float o[8];
+      float (&x)[8] = xh[kAhead ? i : 0], (&v)[8] = d[kAhead ? i : 0];
+      if constexpr (!kAhead) {
+        forget(nx[i]);
+        forget(ny[i]);
+        take(i, x, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = (__builtin_fmaf(-xh[i][j], s2, d[i][j]) - s1) * rstd;
+        for (int j = 0; j < 8; ++j) v[j] *= g[i][j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = (__builtin_fmaf(-x[j], s2, v[j]) - s1) * rstd;
       store8<BF16, VEC, false>(a.dx, row * a.lddx + col[i], ok ? nv[i] : 0, o);
     }
   }
