@@ -83,14 +83,17 @@ bool outputs_overlap(const std::vector<puro::GradJob>& jobs) {
   return false;
 }
 
+inline bool overlap(const void* a, uintptr_t a_bytes, const void* b, uintptr_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
 // Whether [p, p + bytes) shares memory with a tensor of the jobs: such a norm or workspace would be written while
 // other workgroups still read the tensor, or read while they write it.
 bool in_tensors(const std::vector<puro::GradJob>& jobs, const void* p, uintptr_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = lo + bytes;
   for (const puro::GradJob& j : jobs) {
     const uintptr_t n = (uintptr_t)j.n * (j.bf16 ? 2 : 4);
-    const uintptr_t s = reinterpret_cast<uintptr_t>(j.src), d = reinterpret_cast<uintptr_t>(j.dst);
-    if ((lo < s + n && s < hi) || (j.dst && lo < d + n && d < hi)) return true;
+    if (overlap(p, bytes, j.src, n) || (j.dst && overlap(p, bytes, j.dst, n))) return true;
   }
   return false;
 }
@@ -236,6 +239,9 @@ static int grad_common(const puro_grad_job* jobs, int n_jobs, bool clip, float m
   if (parts > 0 && !aligned(workspace, 16)) return PURO_ERR_ALIGN;
   if (clip && in_tensors(b, norm, sizeof(float))) return PURO_ERR_ARG;
   if (parts > 0 && in_tensors(b, workspace, (uintptr_t)parts * sizeof(double))) return PURO_ERR_ARG;
+  // (the scaling's first workgroup writes the norm while others read the partial sums; the norm alone is written
+  // by the one workgroup that has read them)
+  if (clip && overlap(norm, sizeof(float), workspace, (uintptr_t)parts * sizeof(double))) return PURO_ERR_ARG;
   double* w = static_cast<double*>(workspace);
   hipError_t e = puro::launch_grad_squares(b.data(), n, w, st);
   if (e != hipSuccess) return from_hip(e);

@@ -117,7 +117,8 @@ int puro_grad_norm(const puro_grad_job* jobs, int n_jobs, float* norm, void* wor
  * 1 and dst == src nothing is written.  A norm that is not finite is not hidden: an infinite one gives
  * c = 0 (infinite elements become NaN), a NaN makes every element NaN, as the product says.  A dst
  * that overlaps another job's src or dst, or its own src other than being it, is refused (PURO_ERR_ARG):
- * a gradient that is listed twice is one.  So is a norm inside a tensor.
+ * a gradient that is listed twice is one.  So is a norm inside a tensor or inside the part of the workspace
+ * that the call uses.
  */
 int puro_clip_grad_norm(const puro_grad_job* jobs, int n_jobs, float max_norm, float* norm, void* workspace,
                         size_t workspace_bytes, hipStream_t st);

@@ -172,6 +172,15 @@ def test_clip_refuses_a_norm_or_workspace_inside_a_tensor():
     assert P.lib.puro_grad_norm(jobs((A16 + 4, None, 100, FP32)), 1, far, A16, 1 << 20, None) == ARG
 
 
+def test_clip_refuses_a_norm_inside_the_workspace():
+    """The norm is written while other workgroups still read the partial sums, and so do the launches of longer lists."""
+    ws = A16 + (2 << 20)
+    many = [(A16 + 16 * i, A16 + 16 * i, 4, FP32) for i in range(300)]          # three launches, 300 partial sums
+    for at in (ws, ws + 4, ws + 8 * 300 - 4):
+        assert clip(many, norm=at, ws=ws) == ARG
+    assert clip([(A16, A16, 100, FP32)], norm=ws + 4, ws=ws) == ARG
+
+
 def test_grad_workspace_size():
     size = P.lib.puro_grad_norm_workspace_size
     assert size(jobs(), 0) == 0 and size(jobs((A16, None, 0, FP32)), 1) == 0
