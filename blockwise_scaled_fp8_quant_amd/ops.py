@@ -8,9 +8,10 @@ for a non-zero status, nothing launched in either case.  (A dimension of one ele
 as in is_contiguous, and rows may be any distance apart that is no less than their length.)  The marshalling
 itself is native (csrc/marshal.cpp): a decode step makes these calls by the thousand.
 
-Every function takes `stream`: the call then runs as under torch.cuda.stream, so what it allocates (outputs,
-workspace) comes from that stream's memory and is not handed out again before the work on it is done.  A caller that
-uses such an output on another stream orders the two, as for any tensor.
+Every function takes `stream`, a torch stream or a handle as in `cuda_stream` (0 is the default stream's): the call
+then runs as under torch.cuda.stream, so what it allocates (outputs, workspace) comes from that stream's memory and is
+not handed out again before the work on it is done.  A caller that uses such an output on another stream orders the
+two, as for any tensor.
 
 The functions are available from the package.
 """
@@ -83,12 +84,15 @@ _marshal.init(_device, torch._C._cuda_getCurrentRawStream, _raise)
 
 
 def _on(stream, call):
-    """`call`, on the stream named (a torch stream or a raw handle)."""
+    """`call`, on the stream named (a torch stream or a raw handle; ExternalStream takes the handle 0, the default
+    stream's, for none given, and makes a stream that nothing orders)."""
     if stream is None:
         return call
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
 
     def run(*args):
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        with torch.cuda.stream(stream):
             return call(*args)
     return run
 

@@ -233,3 +233,22 @@ def test_binding_refuses_what_the_library_cannot_see():
         P.puro_gemm_rows(x, x, x, x)
     with pytest.raises(ValueError):
         P.puro_gemm_rows(x[0], x, x, x)
+
+
+def test_a_stream_is_taken_for_what_it_is(monkeypatch):
+    """The handle 0 is the default stream's, any other an external stream's; a stream object is itself."""
+    import contextlib
+    import torch
+    from blockwise_scaled_fp8_quant_amd import ops
+    ran = []
+
+    @contextlib.contextmanager
+    def stream(s):
+        ran.append(s)
+        yield
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda *a: "the default stream")
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h: ("external", h))
+    for given, runs in ((0, "the default stream"), (4096, ("external", 4096)), ("an object", "an object")):
+        assert ops._on(given, lambda a, b: (a, b))(1, 2) == (1, 2) and ran.pop() == runs
+    assert ops._on(None, len) is len and not ran
