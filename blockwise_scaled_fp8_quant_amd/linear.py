@@ -34,6 +34,7 @@ import torch
 
 from . import (DGRAD, FWD, OUT_BF16, OUT_FP32, WGRAD, puro_fp8_gemm, puro_fp8_gemm_accumulate,
                puro_fp8_quant_act_1x128, puro_fp8_quant_act_dual, puro_fp8_quant_w_128x128, puro_gemm_rows)
+from ._marshal import check_capture
 
 __all__ = ["Fp8LinearFunction", "Fp8Linear", "fp8_linear"]
 
@@ -43,6 +44,13 @@ def _rows(t: torch.Tensor, width: int) -> torch.Tensor:
     that has no such view, such as a gradient broadcast over the rows)."""
     t2 = t.reshape(-1, width)
     return t2 if t2.stride(1) == 1 and (t2.stride(0) >= width or t2.shape[0] <= 1) else t2.contiguous()
+
+
+def _apply(function, x, *args):
+    """function.apply; a step that is being captured over the living autograd graph of another stream is refused."""
+    if torch.is_grad_enabled() and x.is_cuda and torch.cuda.is_current_stream_capturing():
+        check_capture((x,) + args)
+    return function.apply(x, *args)
 
 
 class Fp8LinearFunction(torch.autograd.Function):
@@ -85,7 +93,7 @@ class Fp8LinearFunction(torch.autograd.Function):
 
 def fp8_linear(x: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
     """Y = X W^T through the blockwise-scaled FP8 path (differentiable)."""
-    return Fp8LinearFunction.apply(x, weight)
+    return _apply(Fp8LinearFunction, x, weight)
 
 
 class Fp8Linear(torch.nn.Module):
@@ -111,7 +119,7 @@ class Fp8Linear(torch.nn.Module):
 
     def forward(self, x: torch.Tensor, codes=None) -> torch.Tensor:
         if codes is None and (torch.is_grad_enabled() or (x.numel() // max(self.in_features, 1)) % 128 == 0):
-            return Fp8LinearFunction.apply(x, self.weight)
+            return _apply(Fp8LinearFunction, x, self.weight)
         if torch.is_grad_enabled():
             raise ValueError("codes: a weight quantized beforehand is for use without gradients (torch.no_grad)")
         if x.dtype != torch.bfloat16:

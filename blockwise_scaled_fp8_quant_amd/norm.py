@@ -25,8 +25,7 @@ from torch.autograd.function import once_differentiable
 from . import (DGRAD, FWD, LAYER_NORM, OUT_BF16, OUT_FP32, RMS_NORM, WGRAD, puro_fp8_gemm, puro_fp8_gemm_accumulate,
                puro_fp8_quant_act_dual, puro_fp8_quant_w_128x128, puro_gemm_rows, puro_layer_norm,
                puro_layer_norm_backward, puro_layer_norm_quant, puro_layer_norm_quant_dual)
-from ._marshal import check_capture
-from .linear import Fp8Linear, _rows
+from .linear import Fp8Linear, _apply, _rows
 
 __all__ = ["Norm", "NormFunction", "Fp8NormLinear", "Fp8NormLinearFunction", "layer_norm", "rms_norm"]
 
@@ -48,12 +47,6 @@ def _norm_grads(kind, dn, x2, gamma, mean, rstd, weight, bias, need_w, need_b):
     if main:
         return dx, None, None
     return dx, dw if need_w else None, db if need_b else None
-
-
-def _apply(function, x, *args):
-    if torch.is_grad_enabled() and x.is_cuda and torch.cuda.is_current_stream_capturing():
-        check_capture((x,) + args)
-    return function.apply(x, *args)
 
 
 class NormFunction(torch.autograd.Function):

@@ -252,3 +252,26 @@ def test_a_stream_is_taken_for_what_it_is(monkeypatch):
     for given, runs in ((0, "the default stream"), (4096, ("external", 4096)), ("an object", "an object")):
         assert ops._on(given, lambda a, b: (a, b))(1, 2) == (1, 2) and ran.pop() == runs
     assert ops._on(None, len) is len and not ran
+
+
+def test_captured_linear_steps_are_checked(monkeypatch):
+    """Every differentiable call made while a graph is recorded is checked before its forward pass starts."""
+    import torch
+    from blockwise_scaled_fp8_quant_amd import linear, norm
+
+    class Stop(Exception):
+        pass
+
+    def check(leaves):
+        raise Stop(len(leaves))
+    monkeypatch.setattr(linear, "check_capture", check)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+
+    class OnGpu(torch.Tensor):
+        is_cuda = True
+    x = torch.zeros((128, 128), dtype=torch.bfloat16).as_subclass(OnGpu)
+    lin, n, both = linear.Fp8Linear(128, 128), norm.Norm(128), norm.Fp8NormLinear(128, 128)
+    for call in (lambda: lin(x), lambda: linear.fp8_linear(x, lin.weight), lambda: n(x), lambda: both(x),
+                 lambda: norm.layer_norm(x, n.weight, n.bias), lambda: norm.rms_norm(x, n.weight)):
+        with pytest.raises(Stop):
+            call()
