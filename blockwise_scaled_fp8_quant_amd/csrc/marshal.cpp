@@ -14,10 +14,13 @@
 #include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/function.h>
+#include <torch/csrc/autograd/functions/accumulate_grad.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/autograd/variable.h>
 
+#include <memory>
 #include <string>
+#include <unordered_set>
 #include <vector>
 
 #include "../../include/puro_ops.h"
@@ -459,25 +462,36 @@ PyObject* gemm_rows(PyObject* const* a) {
   return wrap(C);
 }
 
-// leaves: for the forward pass of a step that is being captured into a graph (the current stream records).  A leaf's
+// tensors: for the forward pass of a step that is being captured into a graph (the current stream records).  A leaf's
 // gradient belongs to the stream that was current when the first graph that reaches it was built, for as long as one of
 // those graphs lives, and the autograd engine joins that stream to the backward pass.  One that does not record breaks
-// the capture from inside the engine, which ends the process: refused here, before the pass starts.
+// the capture from inside the engine, which ends the process: refused here, before the pass starts.  The leaves are the
+// tensors themselves and those that the graphs behind them end in (a view of a leaf, what an earlier layer made of one).
 PyObject* check_capture(PyObject* const* a) {
   if (!PyTuple_Check(a[0])) type_error("expected a tuple of tensors");
+  std::vector<std::shared_ptr<torch::autograd::Node>> todo;
+  std::unordered_set<torch::autograd::Node*> seen;
+  const auto visit = [&](const std::shared_ptr<torch::autograd::Node>& node) {
+    if (node && seen.insert(node.get()).second) todo.push_back(node);
+  };
   for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(a[0]); ++i) {
     PyObject* o = PyTuple_GET_ITEM(a[0], i);
     if (!THPVariable_Check(o)) continue;
     const at::Tensor& t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || !t.requires_grad() || !t.is_leaf()) continue;
-    const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
-    if (!node) continue;
-    const auto st = node->stream();
-    const c10::impl::VirtualGuardImpl guard(t.device().type());
-    if (st && *st != guard.getStream(t.device()))
-      throw Refused{PyExc_RuntimeError,
-                    "a step is being captured while the autograd graph of another stream reaches the same parameter or "
-                    "input: delete the outputs of the earlier passes first"};
+    if (!t.is_cuda() || !t.requires_grad()) continue;
+    visit(t.is_leaf() ? torch::autograd::impl::try_get_grad_accumulator(t) : t.grad_fn());
+  }
+  while (!todo.empty()) {
+    const auto node = todo.back();
+    todo.pop_back();
+    if (dynamic_cast<const torch::autograd::AccumulateGrad*>(node.get())) {
+      const auto st = node->stream();
+      if (st && *st != c10::impl::VirtualGuardImpl(st->device_type()).getStream(st->device()))
+        throw Refused{PyExc_RuntimeError,
+                      "a step is being captured while the autograd graph of another stream reaches the same parameter or "
+                      "input: delete the outputs of the earlier passes first"};
+    }
+    for (const auto& edge : node->next_edges()) visit(edge.function);
   }
   Py_RETURN_NONE;
 }

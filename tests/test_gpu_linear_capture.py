@@ -38,6 +38,35 @@ def test_capture_over_a_living_graph_is_refused(P):
     assert m.weight.grad.isfinite().all() and xin.grad.isfinite().all()
 
 
+def test_capture_over_a_leaf_behind_a_view_is_refused(P):
+    """What is given may be a view of such a leaf, or what an earlier operation made of one."""
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.linear import Fp8Linear
+    from blockwise_scaled_fp8_quant_amd.norm import Norm, rms_norm
+    m, n = Fp8Linear(256, 384, device="cuda"), Norm(256, 0, device="cuda")
+    x = t.randn((2, 64, 256), device="cuda").bfloat16().requires_grad_(True)
+    scale = t.ones(256, device="cuda").bfloat16().requires_grad_(True)
+    fresh = t.randn((128, 256), device="cuda").bfloat16()
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        m(fresh).backward(t.ones((128, 384), device="cuda").bfloat16())
+    t.cuda.current_stream().wait_stream(side)
+    m.weight.grad = None
+    living = (x * 2, scale * 2)
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        for call in (lambda: m(x.view(128, 256)), lambda: n((x + 1).flatten(0, 1)), lambda: rms_norm(fresh, scale.view(256)),
+                     lambda: m((fresh * scale).contiguous())):
+            with pytest.raises(RuntimeError, match="captured"):
+                call()
+        y = m(fresh)                              # nothing living reaches this one
+        y.backward(t.ones_like(y))
+    graph.replay()
+    t.cuda.synchronize()
+    assert m.weight.grad.isfinite().all() and len(living) == 2
+
+
 def test_step_in_a_graph(P):
     """Forward and backward captured together after a pass whose graph is gone; every replay against an eager step."""
     import copy
