@@ -226,15 +226,11 @@ __device__ __forceinline__ void tile_scale32(float amax, float& s, float& r) {
   r = kE4M3Max / a;
 }
 
-// The norm of eight columns for the quantized forms: two FMAs per element, (x r - mu r) g + b, with
-// shift = -mu r.  (The tensor form subtracts the mean first: one rounding less where |mu| is many deviations.
-// Three bits of mantissa do not show it, and the dual form's second launch has many vector instructions.)
-template <bool BF16>
-__device__ __forceinline__ void norm8(const Raw8<BF16>& raw, float rstd, float shift, const float g[8], const float b[8],
-                                      float y[8]) {
-  unpack8<BF16, true>(raw, 8, y);
+// The norm of eight columns: the mean is taken out of x before anything is rounded, so that a row whose values lie far
+// from zero and close together keeps its differences (a constant row's are zero).  v: x - mean.
+__device__ __forceinline__ void norm8(const float v[8], float rstd, const float g[8], const float b[8], float y[8]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(__builtin_fmaf(y[j], rstd, shift), g[j], b[j]);
+  for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(v[j] * rstd, g[j], b[j]);
 }
 
 // max(m, |a|, |b|): one v_max3_f32.  A NaN does not enter (its code is NaN whatever the scale).
@@ -294,12 +290,8 @@ __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void norm_kernel(NormArgs a)
     const int64_t row = row0 + k;
     const bool ok = row < a.T;
     float v[ITER][8];
-    Raw8<BF16> cur[ITER];
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      cur[i] = next[i];
-      unpack8<BF16, VEC>(cur[i], nv[i], v[i]);
-    }
+    for (int i = 0; i < ITER; ++i) unpack8<BF16, VEC>(next[i], nv[i], v[i]);
     if (k + 1 < a.rows_per_team) {
 #pragma unroll
       for (int i = 0; i < ITER; ++i)
@@ -340,12 +332,10 @@ __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void norm_kernel(NormArgs a)
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
         float y[8];
+        norm8(v[i], rstd, g[i], b[i], y);
         if constexpr (WHAT == 0) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(v[i][j] * rstd, g[i][j], b[i][j]);
           store8<BF16, VEC, true>(a.y, row * a.ldy + col[i], ok ? nv[i] : 0, y);
         } else if constexpr (VEC) {
-          norm8<BF16>(cur[i], rstd, a.layer ? -mean * rstd : 0.f, g[i], b[i], y);
           float m = 0.f;
 #pragma unroll
           for (int j = 0; j < 8; j += 2) m = max3abs(m, y[j], y[j + 1]);
@@ -368,12 +358,12 @@ __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void norm_kernel(NormArgs a)
 // read twice (once per launch): keeping 128 whole rows on one CU for a single read does not fit
 // beyond a few hundred columns.
 // Measured at 16384 x 2048 bf16: 23.5 us (5.6 TB/s of reads and writes together, as a copy).  It was bound by
-// vector instructions first (18 us with neither loads nor stores): the two-FMA norm, three-operand maxima on
-// magnitudes and converts without a register to clear took it from 27.6 us.
+// vector instructions first (18 us with neither loads nor stores): three-operand maxima on magnitudes, converts
+// without a register to clear and a norm of two instructions (three with a mean) took it from 27.6 us.
 // ---------------------------------------------------------------------------------------------------
 constexpr int kDualThreads = 256;
 
-template <bool BF16>
+template <bool BF16, bool LAYER>
 __global__ __launch_bounds__(kDualThreads) void norm_dual_kernel(NormArgs a, int bt_log2) {
   constexpr int kWaves = kDualThreads / 64;
   constexpr int kRows = 128 * 16 / kDualThreads;   // tokens per thread: 8 (x 8 columns)
@@ -404,8 +394,13 @@ __global__ __launch_bounds__(kDualThreads) void norm_dual_kernel(NormArgs a, int
   float cm[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const float rstd = a.rstd[tok0 + i], shift = a.layer ? -a.mean[tok0 + i] * rstd : 0.f;
-    norm8<BF16>(raw[i], rstd, shift, g, be, y[i]);
+    unpack8<BF16, true>(raw[i], 8, y[i]);
+    if constexpr (LAYER) {
+      const float mean = a.mean[tok0 + i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[i][j] -= mean;
+    }
+    norm8(y[i], a.rstd[tok0 + i], g, be, y[i]);
     float m = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; j += 2) m = max3abs(m, y[i][j], y[i][j + 1]);
@@ -731,11 +726,12 @@ hipError_t launch_norm_quant_dual(NormArgs a, hipStream_t st) {
   int bt = 5;   // up to 32 token blocks per run of workgroups: transposed rows are written in 4 KB runs
   while (nb & ((int64_t(1) << bt) - 1)) --bt;
   const dim3 grid((unsigned)(nb * (a.C / 128)));
-  if (a.x_bf16)
-    hipLaunchKernelGGL(norm_dual_kernel<true>, grid, dim3(kDualThreads), 0, st, a, bt);
-  else
-    hipLaunchKernelGGL(norm_dual_kernel<false>, grid, dim3(kDualThreads), 0, st, a, bt);
-  return hipGetLastError();
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(kDualThreads), 0, st, a, bt);
+    return hipGetLastError();
+  };
+  if (a.x_bf16) return a.layer ? go(norm_dual_kernel<true, true>) : go(norm_dual_kernel<true, false>);
+  return a.layer ? go(norm_dual_kernel<false, true>) : go(norm_dual_kernel<false, false>);
 }
 
 // One workgroup per CU, but no more than there are rows for its teams, and beyond 64 no more than one for 8 rows:
