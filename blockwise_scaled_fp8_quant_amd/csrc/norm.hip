@@ -10,8 +10,8 @@
 //
 // Statistics are fp32: a thread adds its at most 32 values of the row in order, then the lanes and waves are joined
 // in a tree; the variance is the mean square of the differences from the mean.  y, dx are rounded
-// once.  dg and db are summed in fp32: at most a few tens of rows in order per thread, then waves and
-// workgroups in a fixed order.
+// once.  dg and db are summed in fp32 in short runs: at most 64 rows in order per thread, at most 64 such sums, then
+// teams and workgroups in a fixed order (norm_bwd_kernel): the error does not grow with T.
 #include "codec.hpp"
 #include "gemm_args.hpp"
 #include "ops_internal.hpp"
@@ -467,10 +467,13 @@ __global__ __launch_bounds__(kDualThreads) void norm_dual_kernel(NormArgs a, int
 // Backward.  Eight waves per workgroup, teams of LPR lanes with a row each; a lane's columns as in the
 // forward kernel.  The weight's and bias's gradient of a thread's columns are summed in registers
 // over the team's rows, then over the workgroup's teams through LDS, and written as the workgroup's
-// partial sums; norm_bwd_reduce_kernel adds those in order.
+// partial sums; norm_bwd_reduce_kernel adds those in order.  After every 64 rows a thread adds its sums to a place of
+// its own in LDS and starts anew: in one run of T / 256 rows the error would grow with T (1024 rows of equal terms
+// 256 half steps of fp32 off).  Inputs of up to 64 rows per team, 16384 at 4097 columns and more, have a single run.
 // Measured, 16384 x 2048 bf16: 35.3 us (5.7 TB/s) + 4.7 for the joining; with four chunks per lane 40.4.
 // ---------------------------------------------------------------------------------------------------
 constexpr int kBwdThreads = 512;
+constexpr int kRun = 64;               // rows a thread adds in order, and sums of such runs
 constexpr int kBwdWaves = kBwdThreads / 64;
 
 template <bool BF16, bool VEC, int LPR, int ITER>
@@ -478,7 +481,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, in
   constexpr int kTeams = kBwdThreads / LPR;
   constexpr int kWidth = 8 * LPR * ITER;
   __shared__ float red[2][2][kBwdWaves];
-  __shared__ __attribute__((aligned(16))) float join[kTeams > 1 ? kTeams * kWidth : 4];
+  __shared__ __attribute__((aligned(16))) float join[2][kTeams * kWidth];   // the weight's sums, the bias's
   const int team = threadIdx.x / LPR;
   const int tt = threadIdx.x % LPR;
   const int64_t stride = (int64_t)gridDim.x * kTeams;
@@ -506,6 +509,13 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, in
     }
     nmean = ok && a.layer ? a.mean[r] : 0.f;
     nrstd = ok ? a.rstd[r] : 0.f;
+  };
+  // a thread's eight sums at its place in LDS, set or added to (no other thread touches it before the join)
+  auto put = [&](int which, int i, const float (&v)[8], bool add) {
+    f32x4* p = reinterpret_cast<f32x4*>(join[which] + team * kWidth + col[i]);
+    const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+    p[0] = add ? p[0] + lo : lo;
+    p[1] = add ? p[1] + hi : hi;
   };
   // The widest class has no registers for a row ahead nor for a row's differences between their two uses: it keeps the row
   // as loaded and takes them again (2000 x 16384: bf16 65 us, fp32 110; 88 and 201 as the others do it, spilling).
@@ -572,30 +582,34 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, in
       for (int j = 0; j < 8; ++j) o[j] = (__builtin_fmaf(-x[j], s2, v[j]) - s1) * rstd;
       store8<BF16, VEC, false>(a.dx, row * a.lddx + col[i], ok ? nv[i] : 0, o);
     }
+    if (k % kRun == kRun - 1 && k + 1 < rows_per_team) {   // a run is full, and another one follows
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) {
+        put(0, i, dg[i], k >= kRun);
+        put(1, i, db[i], k >= kRun);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.f;
+      }
+    }
   }
 
-  // the workgroup's sums: first the weight's gradient, then the bias's, through one LDS array
+  // the workgroup's sums: the weight's gradient, then the bias's
   float* out_g = direct ? a.dgamma : a.partial + (int64_t)blockIdx.x * 2 * a.C;
   float* out_b = direct ? a.dbeta : a.partial + ((int64_t)blockIdx.x * 2 + 1) * a.C;
   const bool add = direct && a.accumulate;
+  const bool runs = rows_per_team > kRun;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     float* out = which == 0 ? out_g : out_b;
     if (which == 1 && a.dbeta == nullptr) break;
     if constexpr (kTeams > 1) {
-      if (which == 1) __syncthreads();
 #pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        f32x4* p = reinterpret_cast<f32x4*>(join + team * kWidth + col[i]);
-        const float* v = which == 0 ? dg[i] : db[i];
-        p[0] = f32x4{v[0], v[1], v[2], v[3]};
-        p[1] = f32x4{v[4], v[5], v[6], v[7]};
-      }
+      for (int i = 0; i < ITER; ++i) put(which, i, which == 0 ? dg[i] : db[i], runs);
       __syncthreads();
       for (int c = threadIdx.x; c < a.C; c += kBwdThreads) {
-        float s = join[c];
+        float s = join[which][c];
 #pragma unroll
-        for (int w = 1; w < kTeams; ++w) s += join[w * kWidth + c];
+        for (int w = 1; w < kTeams; ++w) s += join[which][w * kWidth + c];
         out[c] = add ? out[c] + s : s;
       }
     } else {
@@ -603,7 +617,8 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, in
       for (int i = 0; i < ITER; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float s = which == 0 ? dg[i][j] : db[i][j];
+          float s = which == 0 ? dg[i][j] : db[i][j];
+          if (runs) s += join[which][col[i] + j];
           if (j < nv[i]) out[col[i] + j] = add ? out[col[i] + j] + s : s;
         }
     }
@@ -611,22 +626,24 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, in
 }
 
 // dgamma[c], dbeta[c] = sum over workgroups of their partials: 16 columns x 16 runs of workgroups per
-// workgroup, the runs joined in order.
+// workgroup, the runs joined in order.  (More than 256 partials, of more than 10^6 rows, are added in 64 bits 16 at a time.)
 __global__ __launch_bounds__(256) void norm_bwd_reduce_kernel(const float* __restrict__ partial, int blocks, int C,
                                                               float* dgamma, float* dbeta, int accumulate) {
   __shared__ float part[16][17];
   const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
   const int c = blockIdx.x * 16 + cx;
   const int which = blockIdx.y;
-  float s = 0.f;
+  double sum = 0.0;
   if (c < C)
     for (int b0 = ry; b0 < blocks; b0 += 256) {
-      float v[16];
+      float v[16], s = 0.f;
 #pragma unroll
       for (int k = 0; k < 16; ++k) v[k] = b0 + 16 * k < blocks ? partial[((int64_t)(b0 + 16 * k) * 2 + which) * C + c] : 0.f;
 #pragma unroll
       for (int k = 0; k < 16; ++k) s += v[k];
+      sum += (double)s;
     }
+  float s = (float)sum;
   part[ry][cx] = s;
   __syncthreads();
   if (ry == 0 && c < C) {
@@ -739,10 +756,14 @@ hipError_t launch_norm_quant_dual(NormArgs a, hipStream_t st) {
 // row in bf16) is a third of the pass.  A single one, without a second launch, up to two rows per team.  Measured, us:
 // 64 x 2048 7.1 (7.9 with two rows per team at least); 1027 x 4096 14.6 with 128 workgroups, 18.0 with 256; 16 x 1000
 // 5.1 alone, 6.7 in two.
+// Beyond 64 runs of 64 rows for each of 256 workgroups there are more, whole rounds of 256, up to the 2^32 threads of a
+// launch.
 int norm_bwd_blocks(int64_t T, int64_t C) {
   if (T <= 0 || C <= 0) return 0;
   const int64_t teams = kBwdThreads / bwd_lpr(C);
   if (T <= 2 * teams) return 1;
+  const int64_t round = (int64_t)kRun * kRun * 256 * teams;
+  if (T > round) return (int)(256 * std::min<int64_t>((T + round - 1) / round, (int64_t(1) << 32) / (256 * kBwdThreads) - 1));
   return (int)std::min<int64_t>(std::min<int64_t>(256, (T + teams - 1) / teams), std::max<int64_t>(64, (T + 7) / 8));
 }
 

@@ -79,6 +79,8 @@ int puro_layer_norm_quant_dual(int kind, int x_dtype, const void* x, int64_t T, 
  *   mean    : fp32 [T] (NULL for RMS, else PURO_ERR_ARG), rstd: fp32 [T], from the forward pass.
  *   dweight : fp32 [C]; dbias: fp32 [C] or NULL.  accumulate = 0 sets them, 1 adds to them (one fp32
  *             addition per element; for gradients kept over micro-batches).
+ *               Both are fp32 sums of short runs (64 rows, 64 of those sums, up to 32 rows at a time): their
+ *               error does not grow with T.
  *   workspace : puro_layer_norm_backward_workspace_size(T, C) bytes, 16-byte aligned (NULL when 0).
  * T == 0 (or C == 0) writes no dx; with accumulate = 0 it still sets dweight and dbias to zero.
  */

@@ -275,3 +275,14 @@ def test_captured_linear_steps_are_checked(monkeypatch):
                  lambda: norm.layer_norm(x, n.weight, n.bias), lambda: norm.rms_norm(x, n.weight)):
         with pytest.raises(Stop):
             call()
+
+
+def test_norm_backward_workgroups_grow_with_the_rows():
+    """No team takes more than 64 times 64 rows: 8 bytes of partial sums per column and workgroup, 512 threads each, of
+    which one row takes 16 to 512 by its width."""
+    for C, lanes in ((8, 16), (128, 16), (200, 32), (1000, 64), (2000, 128), (4096, 256), (4104, 512), (16384, 512)):
+        teams = 512 // lanes
+        for T in (1000, 16384, 262145, 1 << 20, (1 << 20) + 1, 10 ** 7, 1 << 32):
+            blocks = max(P.puro_layer_norm_backward_workspace_size(T, C) // (8 * C), 1)
+            assert blocks * teams * 4096 >= T and blocks * 512 < 1 << 32
+            assert blocks <= 256 or T > 256 * 4096 * teams
