@@ -18,6 +18,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/autograd/variable.h>
 
+#include <limits>
 #include <memory>
 #include <string>
 #include <unordered_set>
@@ -265,8 +266,9 @@ struct NormIn {
 
 struct Stats {
   at::Tensor mean, rstd;
-  Stats(const Call& c, PyObject* m, PyObject* r, int kind, int64_t T, bool make) {
-    const Shape v{T};
+  Stats(const Call& c, PyObject* m, PyObject* r, const NormIn& n, bool make) {
+    const Shape v{n.T};
+    const int kind = n.kind;
     if (m != Py_None) {
       if (kind == PURO_NORM_RMS) value_error("mean: an RMS norm has none");
       mean = c.whole(m, "mean", at::kFloat, &v);
@@ -277,7 +279,18 @@ struct Stats {
       rstd = c.whole(r, "rstd", at::kFloat, &v);
     else if (make)
       rstd = c.make(v, at::kFloat);
+    columns = n.C > 0;
   }
+
+  // Rows of no columns: the library writes nothing, and their statistics are 0 / 0.
+  void of_nothing() const {
+    if (columns) return;
+    for (const at::Tensor& t : {mean, rstd})
+      if (t.defined()) t.fill_(std::numeric_limits<float>::quiet_NaN());
+  }
+
+ private:
+  bool columns;
 };
 
 // x, weight, bias, eps, kind, y, mean, rstd, stats
@@ -286,12 +299,13 @@ PyObject* layer_norm(PyObject* const* a) {
   NormIn n(c, a);
   int64_t ldy;
   const at::Tensor y = c.out_rows(a[5], "y", n.xt, {n.T, n.C}, ldy);
-  const Stats s(c, a[6], a[7], n.kind, n.T, as_bool(a[8]));
+  const Stats s(c, a[6], a[7], n, as_bool(a[8]));
   const hipStream_t st = c.stream();
   enqueue("puro_layer_norm", [&] {
     return puro_layer_norm(n.kind, n.xd, ptr(n.x), n.T, n.C, n.ldx, n.wd, ptr(n.weight), ptr(n.bias), n.eps, ptr(y), ldy,
                            fptr(s.mean), fptr(s.rstd), st);
   });
+  s.of_nothing();
   return wrap_all(y, s.mean, s.rstd);
 }
 
@@ -302,12 +316,13 @@ PyObject* layer_norm_quant(PyObject* const* a) {
   int64_t ldq;
   const at::Tensor q = c.out_rows(a[5], "q", at::kByte, {n.T, n.C}, ldq);
   const at::Tensor s = c.out_whole(a[6], "s", at::kFloat, {n.C / 128, n.T});
-  const Stats k(c, a[7], a[8], n.kind, n.T, false);
+  const Stats k(c, a[7], a[8], n, false);
   const hipStream_t st = c.stream();
   enqueue("puro_layer_norm_quant", [&] {
     return puro_layer_norm_quant(n.kind, n.xd, ptr(n.x), n.T, n.C, n.ldx, n.wd, ptr(n.weight), ptr(n.bias), n.eps,
                                  static_cast<uint8_t*>(ptr(q)), ldq, fptr(s), fptr(k.mean), fptr(k.rstd), st);
   });
+  k.of_nothing();
   return wrap_all(q, s);
 }
 
@@ -320,13 +335,14 @@ PyObject* layer_norm_quant_dual(PyObject* const* a) {
   const at::Tensor s = c.out_whole(a[6], "s", at::kFloat, {n.C / 128, n.T});
   const at::Tensor qT = c.out_rows(a[7], "qT", at::kByte, {n.C, n.T}, ldqT);
   const at::Tensor sT = c.out_whole(a[8], "sT", at::kFloat, {n.T / 128, n.C});
-  const Stats k(c, a[9], a[10], n.kind, n.T, true);
+  const Stats k(c, a[9], a[10], n, true);
   const hipStream_t st = c.stream();
   enqueue("puro_layer_norm_quant_dual", [&] {
     return puro_layer_norm_quant_dual(n.kind, n.xd, ptr(n.x), n.T, n.C, n.ldx, n.wd, ptr(n.weight), ptr(n.bias), n.eps,
                                       static_cast<uint8_t*>(ptr(q)), ldq, fptr(s), static_cast<uint8_t*>(ptr(qT)), ldqT,
                                       fptr(sT), fptr(k.mean), fptr(k.rstd), st);
   });
+  k.of_nothing();
   return wrap_all(q, s, qT, sT, k.mean, k.rstd);
 }
 

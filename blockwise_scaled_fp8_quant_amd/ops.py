@@ -101,7 +101,7 @@ def puro_layer_norm(x, weight, bias=None, eps: float = 1e-5, kind: int = LAYER_N
                     stats: bool = True, stream=None):
     """x [T, C] bf16 or fp32 -> (y [T, C] of x's type, mean fp32 [T], rstd fp32 [T]): the layer or RMS norm
     of each row and the statistics its backward pass takes.  mean is None for RMS_NORM; with stats=False
-    only the statistics given are written.  y may be x."""
+    only the statistics given are written; those of rows without columns are NaN.  y may be x."""
     return _on(stream, _marshal.layer_norm)(x, weight, bias, eps, kind, y, mean, rstd, stats)
 
 

@@ -36,7 +36,7 @@ enum { PURO_NORM_LAYER = 0, PURO_NORM_RMS = 1 };
  *   eps    : finite, >= 0 (else PURO_ERR_ARG).
  *   y      : [T, C] of x_dtype, row stride ldy.  y may be x (same pointer and stride).
  *   mean, rstd : fp32 [T], the row statistics the backward pass takes; each optional (NULL).  RMS has
- *            no mean: mean must be NULL (else PURO_ERR_ARG).
+ *            no mean: mean must be NULL (else PURO_ERR_ARG).  With C == 0 nothing is written, these included.
  * Mean and variance are taken in fp32 from the row held in registers (variance of the differences
  * from the mean, not of squares), y is rounded once.  Rows need only element alignment (2 or 4
  * bytes, any ldx >= C); 16-byte aligned rows with C % 8 == 0 take the fast path.
