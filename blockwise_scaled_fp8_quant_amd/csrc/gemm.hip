@@ -453,13 +453,6 @@ static hipError_t launch_one(const GemmArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// FWD and DGRAD (without the fused output quantization) run the four-wave kernel of gemm_w4.hip
-// wherever its 32-bit operand offsets reach (w4_supported), the eight-wave kernel elsewhere.
-#ifndef PURO_GEMM_W4
-#define PURO_GEMM_W4 1
-#endif
-constexpr bool kUseW4 = PURO_GEMM_W4 != 0;
-
 // Tile rows per group (see block_of).  The A rows of a group take group x 256 x K bytes of
 // the XCD's 4 MB L2.  Up to K = 2048, 4 rows (2 MB) stay resident from one wave of tiles to
 // the next while the B columns stream past, and 8 rows (4 MB) would not (measured on MI355X at

@@ -80,6 +80,13 @@ __host__ __device__ inline int pf_share_a(const GemmArgs& p) {
 __host__ __device__ inline int pf_share_b(const GemmArgs& p) { return pf_share(p.group < p.tiles_m ? p.group : p.tiles_m); }
 __host__ __device__ inline int pf_row(int lane, int tile, int n) { return (lane & ~(n - 1)) + (tile & (n - 1)); }
 
+// FWD and DGRAD (without the fused output quantization) run the four-wave kernel of gemm_w4.hip
+// wherever its 32-bit operand offsets reach (w4_supported), the eight-wave kernel elsewhere.
+#ifndef PURO_GEMM_W4
+#define PURO_GEMM_W4 1
+#endif
+constexpr bool kUseW4 = PURO_GEMM_W4 != 0;
+
 hipError_t launch_w4(const GemmArgs& a, bool out_bf16, hipStream_t st);
 // Whether launch_w4 can take these arguments: its operand offsets are 32-bit buffer offsets.
 bool w4_supported(const GemmArgs& a);

@@ -267,6 +267,19 @@ int64_t leading_rows(int64_t M, int64_t N, int64_t K) {
   return (double)rows * (double)N * (double)K >= (double)(int64_t(1) << 33) ? rows : 0;
 }
 
+// Whether the blockwise GEMM can read the row scales where they are.  Its four-wave kernel takes them a value at a time; where
+// its 32-bit offsets do not reach, the eight-wave one copies four at once and needs every slice on 16 bytes, which an M
+// that is no multiple of 4, or an sA on 4 bytes, does not give.  (Those calls run here: 2 GiB of weight rows and more.)
+bool scales_reachable(int64_t M, int64_t K, int64_t lda, const float* sA, int64_t ldb) {
+  if (M % 4 == 0 && (reinterpret_cast<uintptr_t>(sA) & 15u) == 0) return true;
+  GemmArgs a = {};
+  a.K = (int)K;
+  a.lda = lda;
+  a.ldb = ldb;
+  a.ldsa = M;
+  return kUseW4 && w4_supported(a);
+}
+
 }  // namespace
 
 size_t gemm_rows_workspace_bytes(int64_t M, int64_t N, int64_t K) {
@@ -277,7 +290,8 @@ size_t gemm_rows_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 hipError_t launch_gemm_rows(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda, const float* sA,
                             const uint8_t* B, int64_t ldb, const float* sB, void* C, int64_t ldc, bool out_bf16,
                             void* workspace, size_t workspace_bytes, hipStream_t st) {
-  const int64_t lead = out_bf16 ? leading_rows(M, N, K) : 0;
+  int64_t lead = out_bf16 ? leading_rows(M, N, K) : 0;
+  if (lead && !scales_reachable(M, K, lda, sA, ldb)) lead = 0;
   if (lead) {
     const hipError_t e = launch_gemm(0, lead, N, K, A, lda, sA, B, ldb, sB, C, ldc, true, false, nullptr, 0, nullptr,
                                      workspace, workspace_bytes, st, M);
