@@ -19,8 +19,10 @@
 // for a slice ahead beyond 32 rows and 3 strips (200 x 6144 deep x 2048, same tile: 14.3 us so, 12.9 as it is).
 //
 // The codes are converted, exactly, to bf16, whose matrix instruction keeps a full fp32 sum (1e-7 off, relative); the
-// FP8 one's sum of 128 products is about 1.4e-5 off, which an fp32 output shows and a sum that cancels shows in
-// bf16 too.  The conversion costs 2 to 9% up to 64 rows and 6 to 11% at 200, where matrix work shows.  (Its
+// FP8 one's sum of 128 products is 1.4e-5 off (normal data; 5e-5 for codes of every magnitude, a single sum up to 1.6e-4
+// of its magnitudes), which an fp32 output shows and a sum that cancels shows in bf16 too.  The leading rows of a long
+// bf16 product, which the FP8 ones take (leading_rows), are as far off as the blockwise GEMM's, and up to three times as
+// fast.  The conversion costs 2 to 9% up to 64 rows and 6 to 11% at 200, where matrix work shows.  (The FP8 one's
 // 16 x 16 x 32 form is 9e-5 off.)
 // The weight is the first operand: a lane then holds four consecutive columns of one output row, and
 // its row scale is one value.
@@ -260,11 +262,16 @@ hipError_t by_tile(const RowsArgs& a, bool out_bf16, hipStream_t st) {
 }
 
 // Leading rows (a multiple of 128) that go through the 256 x 256 tiles of the blockwise GEMM: all there are, where their
-// product is long enough to fill it.  Both sides, us: 512 x 12288 x 2048 42 here, 26 there; 1024 x 4096 x 2048 28 and
-// 27; 256 x 12288 x 2048 24 and 27; 512 x 2048 x 6144 22 and 30; 2048 x 1024 x 1024 10 and 15.
+// product is long enough to fill it.  The rows left over then read the weight once more, and 128 leading rows fill half a
+// row of tiles, so those need twice the product.  Both sides, us (all rows here; leading rows there and the rest here):
+//   256 rows and more: 512 x 12288 x 2048 42.2, 25.8; 500 41.4, 41.5; 1024 x 4096 x 2048 27.8, 27.4; 1025 31.0, 31.0;
+//   300 x 32768 x 2048 73, 45; 257 x 8192 x 8192 60.8, 55.6; below 2^33: 256 x 12288 x 2048 22.5, 25.2; 257 28.0, 30.9;
+//   640 x 2048 x 6144 27, 29; 2048 x 1024 x 1024 10, 15
+//   128 to 255 rows: 128 x 151936 x 2048 172, 95; 200 310, 216; 255 318, 240; below 2^34: 130 x 8192 x 8192 37.8, 44.1; 255
+//   48.7, 57.6; 130 x 32768 x 2048 43.3, 45.6; 128 x 12288 x 6144 36.6, 36.0; 255 60.5, 64.1
 int64_t leading_rows(int64_t M, int64_t N, int64_t K) {
   const int64_t rows = M - M % 128;
-  return (double)rows * (double)N * (double)K >= (double)(int64_t(1) << 33) ? rows : 0;
+  return (double)rows * (double)N * (double)K >= (double)(int64_t(1) << (rows < 256 ? 34 : 33)) ? rows : 0;
 }
 
 // Whether the blockwise GEMM can read the row scales where they are.  Its four-wave kernel takes them a value at a time; where

@@ -143,10 +143,13 @@ size_t puro_grad_norm_workspace_size(const puro_grad_job* jobs, int n_jobs);
  *         M, K < 2^31, N < 2^29, lda, ldb <= 2^29 (else PURO_ERR_UNSUPPORTED).
  *   workspace : puro_gemm_rows_workspace_size(M, N, K) bytes, 16-byte aligned (NULL when 0); an fp32 output needs
  *         none.
- * Alignment as puro_fp8_gemm (16-byte pointers and row strides; sA and sB 4-byte).  Codes are decoded exactly to bf16 and
- * multiplied by bf16 matrix instructions with fp32 sums, each 128-deep slice scaled into a separate
- * fp32 accumulator.  Of a long bf16 product (2^33 multiplications or more) the leading multiple of 128 rows
- * is what puro_fp8_gemm writes for them, with its FP8 matrix instructions' sums.
+ * Alignment as puro_fp8_gemm (16-byte pointers and row strides; sA and sB 4-byte).  Codes are decoded exactly to bf16
+ * and multiplied by bf16 matrix instructions with fp32 sums, each 128-deep slice scaled into a separate fp32
+ * accumulator (measured up to 3e-7 of the sum of magnitudes off).  Of a long bf16 product the leading multiple of 128
+ * rows is what puro_fp8_gemm writes for them, with its FP8 matrix instructions' sums (up to 1.6e-4): from 2^33
+ * multiplications of at least 256 leading rows, 2^34 of 128 (weights that puro_fp8_gemm's 32-bit offsets do not reach
+ * excepted).  An fp32 output has the row kernel's sums throughout.  The last bits of a row depend on M in any case: the
+ * order of the sums goes by the tile.
  */
 int puro_gemm_rows(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda, const float* sA, const uint8_t* B,
                    int64_t ldb, const float* sB, void* C, int64_t ldc, int out_dtype, void* workspace,

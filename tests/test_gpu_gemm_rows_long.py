@@ -34,3 +34,18 @@ def test_row_scales_on_four_bytes(P):
     off = t.empty(sA.numel() + 1, device="cuda")[1:].view(sA.shape)
     off.copy_(sA)
     assert off.data_ptr() % 16 == 4 and t.equal(P.puro_gemm_rows(A, off, B, sB), P.puro_fp8_gemm(P.FWD, A, sA, B, sB))
+
+
+@pytest.mark.parametrize("M", [128, 130, 200, 255])
+def test_half_a_row_of_tiles_needs_twice_the_product(P, M):
+    """128 to 255 rows: the blockwise GEMM takes 128 of them from 2^34 multiplications; below, every row keeps the row
+    kernel's bound."""
+    t = torch()
+    A, sA, B, sB = operands(M, 8192, 8192, M)
+    say(f"[rows, half a tile row] {M}x8192x8192")
+    check(P, A, sA, B, sB, P.puro_gemm_rows(A, sA, B, sB), t.bfloat16, "below")
+    A, sA, B, sB = operands(M, 16384, 8192, M)
+    C = P.puro_gemm_rows(A, sA, B, sB)
+    assert t.equal(C[:128], P.puro_fp8_gemm(P.FWD, A[:128], sA[:, :128].contiguous(), B, sB))
+    if M > 128:
+        check(P, A[128:], sA[:, 128:].contiguous(), B, sB, C[128:], t.bfloat16, "rest")

@@ -286,3 +286,13 @@ def test_norm_backward_workgroups_grow_with_the_rows():
             blocks = max(P.puro_layer_norm_backward_workspace_size(T, C) // (8 * C), 1)
             assert blocks * teams * 4096 >= T and blocks * 512 < 1 << 32
             assert blocks <= 256 or T > 256 * 4096 * teams
+
+
+def test_rows_workspace_follows_the_leading_rows():
+    """The blockwise GEMM's workspace for the rows that it takes: 256 and more from 2^33 multiplications, 128 from 2^34."""
+    size, gemm = P.puro_gemm_rows_workspace_size, lambda M, N, K: P.puro_fp8_gemm_workspace_size(P.FWD, M, N, K)
+    assert gemm(128, 8192, 8192) > 0 and gemm(256, 4096, 8192) > 0
+    for M in (128, 130, 255):
+        assert size(M, 8192, 8192) == 0 and size(M, 8192, 16384) == gemm(128, 8192, 16384) > 0
+    for M in (256, 257, 383):
+        assert size(M, 4096, 8192) == gemm(256, 4096, 8192) and size(M, 4096, 8064) == 0
