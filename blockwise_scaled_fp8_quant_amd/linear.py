@@ -23,8 +23,9 @@ autograd stores it in the weight's dtype.
 
 Shapes follow the kernels: Din, Dout and the number of tokens (product of X's leading
 dimensions) must be multiples of 128; anything else raises PuroError (PURO_ERR_SHAPE).  Without
-gradients (torch.no_grad) the number of tokens is free: a ragged one runs puro_gemm_rows, and so
-does a caller that keeps the weight's codes over many calls (Fp8Linear.quantize_weight).
+gradients (torch.no_grad) Fp8Linear makes the forward codes alone and the number of tokens is free: a
+multiple of 128 runs FWD as above, a ragged one puro_gemm_rows, and so does a caller that keeps the
+weight's codes over many calls (Fp8Linear.quantize_weight).
 """
 from __future__ import annotations
 
@@ -118,17 +119,22 @@ class Fp8Linear(torch.nn.Module):
         return puro_fp8_quant_w_128x128(_rows(self.weight.detach(), self.in_features), transposed=False)[:2]
 
     def forward(self, x: torch.Tensor, codes=None) -> torch.Tensor:
-        if codes is None and (torch.is_grad_enabled() or (x.numel() // max(self.in_features, 1)) % 128 == 0):
-            return _apply(Fp8LinearFunction, x, self.weight)
         if torch.is_grad_enabled():
-            raise ValueError("codes: a weight quantized beforehand is for use without gradients (torch.no_grad)")
-        if x.dtype != torch.bfloat16:
+            if codes is not None:
+                raise ValueError("codes: a weight quantized beforehand is for use without gradients (torch.no_grad)")
+            return _apply(Fp8LinearFunction, x, self.weight)
+        if x.dtype != torch.bfloat16 or (codes is None and self.weight.dtype != torch.bfloat16):
             raise TypeError("Fp8Linear takes bf16 activations and bf16 weights")
         if x.shape[-1] != self.in_features:
             raise ValueError(f"x has {x.shape[-1]} features, weight expects {self.in_features}")
+        x2 = _rows(x, self.in_features)
+        xq, xs = puro_fp8_quant_act_1x128(x2)
         wq, ws = self.quantize_weight() if codes is None else codes
-        xq, xs = puro_fp8_quant_act_1x128(_rows(x, self.in_features))
-        return puro_gemm_rows(xq, xs, wq, ws).view(*x.shape[:-1], self.out_features)
+        if codes is None and x2.shape[0] % 128 == 0:
+            y = puro_fp8_gemm(FWD, xq, xs, wq, ws)         # the differentiable call's result, without the codes of its backward
+        else:
+            y = puro_gemm_rows(xq, xs, wq, ws)
+        return y.view(*x.shape[:-1], self.out_features)
 
     def extra_repr(self) -> str:
         return f"in_features={self.in_features}, out_features={self.out_features}, fp8=blockwise"
