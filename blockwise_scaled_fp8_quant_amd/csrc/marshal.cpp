@@ -193,6 +193,14 @@ void enqueue(const char* where, F f) {
   }
 }
 
+// A tensor of the caller's (o, None if the call made its own) has been written: raises its version, by which autograd
+// notices that one it has saved is not what it was.  (Those made in inference mode have none.)
+void written(PyObject* o) {
+  if (o == Py_None) return;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* wrap(const at::Tensor& t) {
   if (!t.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(t);
@@ -306,6 +314,7 @@ PyObject* layer_norm(PyObject* const* a) {
                            fptr(s.mean), fptr(s.rstd), st);
   });
   s.of_nothing();
+  for (int i : {5, 6, 7}) written(a[i]);
   return wrap_all(y, s.mean, s.rstd);
 }
 
@@ -323,6 +332,7 @@ PyObject* layer_norm_quant(PyObject* const* a) {
                                  static_cast<uint8_t*>(ptr(q)), ldq, fptr(s), fptr(k.mean), fptr(k.rstd), st);
   });
   k.of_nothing();
+  for (int i : {5, 6, 7, 8}) written(a[i]);
   return wrap_all(q, s);
 }
 
@@ -343,6 +353,7 @@ PyObject* layer_norm_quant_dual(PyObject* const* a) {
                                       fptr(sT), fptr(k.mean), fptr(k.rstd), st);
   });
   k.of_nothing();
+  for (int i : {5, 6, 7, 8, 9, 10}) written(a[i]);
   return wrap_all(q, s, qT, sT, k.mean, k.rstd);
 }
 
@@ -379,6 +390,7 @@ PyObject* layer_norm_backward(PyObject* const* a) {
     return puro_layer_norm_backward(kind, xd, ptr(dy), lddy, ptr(x), ldx, T, C, wd, ptr(weight), fptr(mean), fptr(rstd),
                                     ptr(dx), lddx, fptr(dw), fptr(db), accumulate ? 1 : 0, ptr(ws), bytes, st);
   });
+  for (int i : {6, 7, 8}) written(a[i]);
   return wrap_all(dx, dw, db);
 }
 
@@ -416,6 +428,12 @@ std::vector<puro_grad_job> grad_jobs(const Call& c, PyObject* grads, PyObject* o
   return jobs;
 }
 
+// The gradients, or their outputs, have been scaled.
+void scaled(PyObject* grads, PyObject* outs) {
+  PyObject* list = outs == Py_None ? grads : outs;
+  for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(list); ++i) written(PySequence_Fast_GET_ITEM(list, i));
+}
+
 at::Tensor norm_value(const Call& c, PyObject* o) {
   if (o == Py_None) return c.make({}, at::kFloat);
   const at::Tensor t = c.whole(o, "norm", at::kFloat, nullptr);
@@ -438,6 +456,8 @@ PyObject* clip_grad_norm(PyObject* const* a) {
     enqueue("puro_clip_grad_norm", [&] { return puro_clip_grad_norm(jobs.data(), n, max_norm, fptr(norm), ptr(ws), bytes, st); });
   else
     enqueue("puro_grad_norm", [&] { return puro_grad_norm(jobs.data(), n, fptr(norm), ptr(ws), bytes, st); });
+  if (clip) scaled(a[0], a[2]);
+  written(a[3]);
   return wrap(norm);
 }
 
@@ -450,6 +470,7 @@ PyObject* scale_by_norm(PyObject* const* a) {
   const at::Tensor norm = norm_value(c, a[2]);
   const hipStream_t st = c.stream();
   enqueue("puro_scale_by_norm", [&] { return puro_scale_by_norm(jobs.data(), (int)jobs.size(), max_norm, fptr(norm), st); });
+  scaled(a[0], a[3]);
   Py_RETURN_NONE;
 }
 
@@ -475,6 +496,7 @@ PyObject* gemm_rows(PyObject* const* a) {
     return puro_gemm_rows(M, N, K, static_cast<const uint8_t*>(ptr(A)), lda, fptr(sA), static_cast<const uint8_t*>(ptr(B)), ldb,
                           fptr(sB), ptr(C), ldc, (int)od, ptr(ws), bytes, st);
   });
+  written(a[4]);
   return wrap(C);
 }
 
