@@ -90,14 +90,13 @@ def build(verbose: bool = True) -> str:
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         marshal = ex.submit(_compile_marshal)
         objs = list(ex.map(_compile, SOURCES))
-        marshal_obj = marshal.result()
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", "-mcode-object-version=5", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_marshal(marshal_obj)
+    _link_marshal(marshal.result())     # (where torch's headers do not compile, the library is there all the same)
     if verbose:
         print(f"built {LIB} and {os.path.basename(MARSHAL)}")
     return LIB

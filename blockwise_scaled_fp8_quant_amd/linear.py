@@ -35,7 +35,7 @@ import torch
 
 from . import (DGRAD, FWD, OUT_BF16, OUT_FP32, WGRAD, puro_fp8_gemm, puro_fp8_gemm_accumulate,
                puro_fp8_quant_act_1x128, puro_fp8_quant_act_dual, puro_fp8_quant_w_128x128, puro_gemm_rows)
-from ._marshal import check_capture
+from .ops import check_capture
 
 __all__ = ["Fp8LinearFunction", "Fp8Linear", "fp8_linear"]
 

@@ -18,16 +18,28 @@ The functions are available from the package.
 from __future__ import annotations
 
 import ctypes
-import os
 
 import torch
 
 from . import OUT_BF16, PuroError, _i64, _int, _p, _sz, lib
 
-if not os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_marshal.so")):
-    raise ImportError("_marshal.so is missing beside ops.py: build it first (python "
-                      "blockwise_scaled_fp8_quant_amd/build.py or __graft_entry__.build())")
-from . import _marshal  # noqa: E402
+
+class _Unavailable:
+    """In the place of the marshalling where it is not built or does not load: the entry points of puro_fp8.h work
+    without it, those here say what is missing."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"_marshal.so beside ops.py is needed for this call ({self._why}): build it (python "
+                          "blockwise_scaled_fp8_quant_amd/build.py or __graft_entry__.build())")
+
+
+try:
+    from . import _marshal
+except ImportError as _error:
+    _marshal = _Unavailable(_error)
 
 __all__ = [
     "LAYER_NORM", "RMS_NORM", "EXPORTED_OPS", "GradJob", "puro_layer_norm", "puro_layer_norm_quant",
@@ -80,7 +92,14 @@ def _raise(status: int, where: str):
     raise PuroError(status, where)
 
 
-_marshal.init(_device, torch._C._cuda_getCurrentRawStream, _raise)
+if not isinstance(_marshal, _Unavailable):
+    _marshal.init(_device, torch._C._cuda_getCurrentRawStream, _raise)
+
+
+def check_capture(tensors):
+    """Refuse (RuntimeError) a step that is being captured over the living autograd graph of another stream, which would
+    end the process; tensors: the inputs and parameters of a differentiable call."""
+    _marshal.check_capture(tensors)
 
 
 def _on(stream, call):
