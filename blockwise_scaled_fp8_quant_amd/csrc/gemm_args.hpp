@@ -80,6 +80,17 @@ __host__ __device__ inline int pf_share_a(const GemmArgs& p) {
 __host__ __device__ inline int pf_share_b(const GemmArgs& p) { return pf_share(p.group < p.tiles_m ? p.group : p.tiles_m); }
 __host__ __device__ inline int pf_row(int lane, int tile, int n) { return (lane & ~(n - 1)) + (tile & (n - 1)); }
 
+// Bytes that a buffer resource of the four-wave kernels reaches, from a tile's first operand row to the last code, and from
+// its first row scale to the last one, that belong to the matrix.  Tiles may hang over the last row and prefetches run two
+// slices ahead; reads past these bytes return 0, also where a launch covers the last of the matrix's rows (slices of sA
+// are then further apart than its rows) or rows are further apart than their codes.
+__host__ __device__ inline int64_t tile_bytes(int rows_left, int64_t ld, int K) {
+  return (int64_t)((rows_left < 256 ? rows_left : 256) - 1) * ld + K;
+}
+__host__ __device__ inline int64_t scale_bytes(int rows_left, int64_t ldsa, int K) {
+  return ((int64_t)(K / 128 - 1) * ldsa + (rows_left < 256 ? rows_left : 256)) * 4;
+}
+
 // FWD and DGRAD (without the fused output quantization) run the four-wave kernel of gemm_w4.hip
 // wherever its 32-bit operand offsets reach (w4_supported), the eight-wave kernel elsewhere.
 #ifndef PURO_GEMM_W4

@@ -210,9 +210,9 @@ void gemm_w4_kernel(GemmArgs p) {
   const int kb_end = min(kb_begin + p.kb_per_split, nk);
 
   // ---- copy operands (see gen_w4_asm.py): buffer resources over the tile's valid rows
-  const w4_v4i rA = rsrc(p.A + (int64_t)m0 * p.lda, (int64_t)min(256, p.M - m0) * p.lda);
-  const w4_v4i rB = rsrc(p.B + (int64_t)n0 * p.ldb, (int64_t)min(256, p.N - n0) * p.ldb);
-  const w4_v4i rS = rsrc(p.sA + m0, ((int64_t)nk * p.ldsa - m0) * 4);
+  const w4_v4i rA = rsrc(p.A + (int64_t)m0 * p.lda, tile_bytes(p.M - m0, p.lda, p.K));
+  const w4_v4i rB = rsrc(p.B + (int64_t)n0 * p.ldb, tile_bytes(p.N - n0, p.ldb, p.K));
+  const w4_v4i rS = rsrc(p.sA + m0, scale_bytes(p.M - m0, p.ldsa, p.K));
   const w4_v4i rW = rsrc(p.sB + (int64_t)(n0 >> 7) * nk, (int64_t)((p.N >> 7) - (n0 >> 7)) * nk * 4);
   w4_v8i qa, qb;                                   // the wave's 8-row copy groups
 #pragma unroll
@@ -313,9 +313,9 @@ void gemm_w4mx_kernel(GemmArgs p) {
 
   // ---- copy operands (see gen_w4mx_asm.py): buffer resources over the tile's valid rows; the scale
   // arrays hold 4 bytes (one slice's 4 block scales) per row
-  const w4_v4i rA = rsrc(p.A + (int64_t)m0 * p.lda, (int64_t)min(256, p.M - m0) * p.lda);
-  const w4_v4i rB = rsrc(p.B + (int64_t)n0 * p.ldb, (int64_t)min(256, p.N - n0) * p.ldb);
-  const w4_v4i rS = rsrc(p.sA + m0, ((int64_t)nk * p.ldsa - m0) * 4);
+  const w4_v4i rA = rsrc(p.A + (int64_t)m0 * p.lda, tile_bytes(p.M - m0, p.lda, p.K));
+  const w4_v4i rB = rsrc(p.B + (int64_t)n0 * p.ldb, tile_bytes(p.N - n0, p.ldb, p.K));
+  const w4_v4i rS = rsrc(p.sA + m0, scale_bytes(p.M - m0, p.ldsa, p.K));
   const w4_v4i rX = rsrc(p.sB + n0, ((int64_t)nk * p.N - n0) * 4);
   w4_v8i qa, qb;
 #pragma unroll
