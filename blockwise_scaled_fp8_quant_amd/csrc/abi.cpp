@@ -233,7 +233,7 @@ const char* puro_fp8_strerror(int status) {
     case PURO_ERR_WORKSPACE: return "workspace too small";
     case PURO_ERR_HIP: return "HIP runtime error at launch";
     case PURO_ERR_UNSUPPORTED: return "request outside what this library implements";
-    case PURO_ERR_ARG: return "argument out of range (eps, max_norm, accumulate, or a mean given to an RMS norm)";
+    case PURO_ERR_ARG: return "argument out of range (eps, max_norm, accumulate), a mean given to an RMS norm, or memory that overlaps";
     default: return "unknown status";
   }
 }

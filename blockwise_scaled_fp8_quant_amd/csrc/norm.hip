@@ -518,7 +518,8 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwdArgs a, in
     p[1] = add ? p[1] + hi : hi;
   };
   // The widest class has no registers for a row ahead nor for a row's differences between their two uses: it keeps the row
-  // as loaded and takes them again (2000 x 16384: bf16 65 us, fp32 110; 88 and 201 as the others do it, spilling).
+  // as loaded and takes them again (2000 x 16384: bf16 65 us, fp32 110; 88 and 201 as the others do it, spilling).  Of its
+  // instances the one of unaligned fp32 rows still spills, 136 bytes a lane.
   constexpr bool kAhead = ITER < 4;
   if (kAhead) fetch(row);
   for (int k = 0; k < rows_per_team; ++k, row += stride) {

@@ -41,7 +41,8 @@ enum { PURO_NORM_LAYER = 0, PURO_NORM_RMS = 1 };
  * from the mean, not of squares), y is rounded once.  Rows need only element alignment (2 or 4
  * bytes, any ldx >= C); 16-byte aligned rows with C % 8 == 0 take the fast path.
  * A NaN or an infinity stays in its row (a layer norm's whole row becomes NaN).  Squares are fp32: beyond about 1e17
- * of |x - mu| their sum leaves its range, rstd is 0 and y is bias.  C > 16384: PURO_ERR_UNSUPPORTED.
+ * of |x - mu| their sum leaves its range, rstd is 0 and y is bias; beyond 2e34 of |x| so does a layer norm's sum, and
+ * the row is NaN.  C > 16384: PURO_ERR_UNSUPPORTED.
  */
 int puro_layer_norm(int kind, int x_dtype, const void* x, int64_t T, int64_t C, int64_t ldx, int w_dtype,
                     const void* weight, const void* bias, float eps, void* y, int64_t ldy, float* mean, float* rstd,
@@ -117,7 +118,8 @@ int puro_grad_norm(const puro_grad_job* jobs, int n_jobs, float* norm, void* wor
  *   c = min(1, max_norm / (norm + 1e-6))
  * in fp32, rounded once to the tensor's type.  max_norm: >= 0, not NaN (else PURO_ERR_ARG).  Where c is
  * 1 and dst == src nothing is written.  A norm that is not finite is not hidden: an infinite one gives
- * c = 0 (infinite elements become NaN), a NaN makes every element NaN, as the product says.  A dst
+ * c = 0 (infinite elements become NaN; where max_norm is infinite too, c and every element), a NaN makes
+ * every element NaN, as the product says.  A dst
  * that overlaps another job's src or dst, or its own src other than being it, is refused (PURO_ERR_ARG):
  * a gradient that is listed twice is one.  So is a norm inside a tensor or inside the part of the workspace
  * that the call uses.
