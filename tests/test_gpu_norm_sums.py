@@ -2,7 +2,7 @@
 
 Tolerance, with u = 2^-24: a thread adds at most 64 rows in order and at most 64 such sums, a workgroup up to 32 of those,
 a run of workgroups 16, and 16 runs are joined; each term has two roundings before its addition, and 64-bit sums between
-16 workgroups and the next are rounded once: (64 + 64 + 32 + 16 + 16 + 3) u sum|terms|."""
+16 workgroups and the next are rounded once: (64 + 64 + 32 + 16 + 16 + 3) u sum|terms|.  (The longest inputs have more than 256 workgroups.)"""
 import pytest
 
 from gpu_util import say, torch
@@ -18,7 +18,7 @@ def P():
     return P
 
 
-@pytest.mark.parametrize("T,C", [(262144, 4104), (262144 * 32, 8), (1 << 20, 2000)])
+@pytest.mark.parametrize("T,C", [(262144, 4104), (262144 * 32, 8), (1 << 20, 2000), ((1 << 25) + 5, 8)])
 def test_terms_that_round_one_way(P, T, C):
     """Terms of 1 + 2^-15 - 2^-23: between 512 and 1024 a sum's step is 2^-14, and each addition there loses nearly half
     of one.  512 such additions in order are 256 u off."""
@@ -35,7 +35,7 @@ def test_terms_that_round_one_way(P, T, C):
     assert none is None and float((dw.double() / (T * term) - 1).abs().max()) <= BOUND
 
 
-@pytest.mark.parametrize("T,C", [(262272, 8192), (70001, 4097), (1000003, 130), (40000, 16384)])
+@pytest.mark.parametrize("T,C", [(262272, 8192), (70001, 4097), (1000003, 130), (40000, 16384), ((1 << 25) + 77, 3), ((1 << 22) + 9, 1030)])
 def test_random_rows(P, T, C):
     t = torch()
     g = t.Generator(device="cuda")
