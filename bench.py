@@ -59,8 +59,9 @@ CSRC = os.path.join(ROOT, "blockwise_scaled_fp8_quant_amd", "csrc")
 COPY_BYTES = 256 << 20          # calibration copy: 256 MiB read + 256 MiB written
 
 
-# operators that no step here launches (norm, clipping, few-row product)
-OTHER_SOURCES = ("clip.hip", "gemm_rows.hip", "norm.hip", "ops_internal.hpp")
+# operators that no step here launches (norm, residual sum, rotary positions, clipping, AdamW, few-row product)
+OTHER_SOURCES = ("adamw.hip", "clip.hip", "gemm_rows.hip", "norm.hip", "ops_internal.hpp", "residual.hip", "rotary.hip",
+                 "rows.hpp")
 
 
 def kernel_source_hash() -> str:

@@ -500,6 +500,335 @@ PyObject* gemm_rows(PyObject* const* a) {
   return wrap(C);
 }
 
+// ---- residual sum and norm ---------------------------------------------------------------------------
+constexpr int kResidualIn = 14;
+
+// h, x, weight, bias, eps, kind, gate, post_weight, scale, h_out, mean, rstd, post_mean, post_rstd: what every forward form
+// takes.  make: statistics that are not given are allocated.
+struct ResidualIn {
+  puro_residual r = {};
+  at::ScalarType xt;
+  at::Tensor h, x, weight, bias, gate, post, h_out, mean, rstd, post_mean, post_rstd;
+  ResidualIn(const Call& c, PyObject* const* a, bool make) {
+    r.kind = norm_kind(a[5]);
+    r.eps = (float)as_float(a[4], "eps");
+    r.scale = (float)as_float(a[8], "scale");
+    r.x_dtype = dtype_code(a[0], "h", xt);
+    h = c.rows(a[0], "h", xt, nullptr, r.ldh);
+    const Shape shape{h.size(0), h.size(1)}, vec{shape[1]}, stat{shape[0]};
+    r.T = shape[0];
+    r.C = shape[1];
+    x = c.rows(a[1], "x", xt, &shape, r.ldx);
+    at::ScalarType wt;
+    r.w_dtype = dtype_code(a[2], "weight", wt);
+    weight = c.whole(a[2], "weight", wt, &vec);
+    if (a[3] != Py_None) bias = c.whole(a[3], "bias", wt, &vec);
+    if (a[6] != Py_None) gate = c.whole(a[6], "gate", wt, &vec);
+    if (a[7] != Py_None) post = c.whole(a[7], "post_weight", wt, &vec);
+    h_out = c.out_rows(a[9], "h_out", xt, shape, r.ldh_out);
+    const bool layer = r.kind == PURO_NORM_LAYER;
+    const auto statistic = [&](PyObject* o, const char* what, bool there, const char* why) {
+      if (o != Py_None && !there) value_error(std::string(what) + why);
+      if (o != Py_None) return at::Tensor(c.whole(o, what, at::kFloat, &stat));
+      return make && there ? c.make(stat, at::kFloat) : at::Tensor();
+    };
+    mean = statistic(a[10], "mean", layer, ": an RMS norm has none");
+    rstd = statistic(a[11], "rstd", true, "");
+    post_mean = statistic(a[12], "post_mean", layer && post.defined(), ": an RMS norm, or no norm of x, has none");
+    post_rstd = statistic(a[13], "post_rstd", post.defined(), ": without post_weight there is no norm of x");
+    r.h = ptr(h);
+    r.x = ptr(x);
+    r.weight = ptr(weight);
+    r.bias = ptr(bias);
+    r.gate = ptr(gate);
+    r.post_weight = ptr(post);
+    r.h_out = ptr(h_out);
+    r.mean = fptr(mean);
+    r.rstd = fptr(rstd);
+    r.post_mean = fptr(post_mean);
+    r.post_rstd = fptr(post_rstd);
+  }
+
+  // After the call: rows of no columns have statistics of 0 / 0, and the caller's tensors are new.
+  void done(PyObject* const* a) const {
+    if (r.C == 0)
+      for (const at::Tensor& t : {mean, rstd, post_mean, post_rstd})
+        if (t.defined()) t.fill_(std::numeric_limits<float>::quiet_NaN());
+    for (int i = 9; i < kResidualIn; ++i) written(a[i]);
+  }
+};
+
+// the above, y, stats
+PyObject* residual_norm(PyObject* const* a) {
+  Call c;
+  const ResidualIn n(c, a, as_bool(a[kResidualIn + 1]));
+  int64_t ldy;
+  const at::Tensor y = c.out_rows(a[kResidualIn], "y", n.xt, {n.r.T, n.r.C}, ldy);
+  const hipStream_t st = c.stream();
+  enqueue("puro_residual_norm", [&] { return puro_residual_norm(&n.r, ptr(y), ldy, st); });
+  n.done(a);
+  written(a[kResidualIn]);
+  return wrap_all(y, n.h_out, n.mean, n.rstd, n.post_mean, n.post_rstd);
+}
+
+// the above, q, s
+PyObject* residual_norm_quant(PyObject* const* a) {
+  Call c;
+  const ResidualIn n(c, a, false);
+  int64_t ldq;
+  const at::Tensor q = c.out_rows(a[kResidualIn], "q", at::kByte, {n.r.T, n.r.C}, ldq);
+  const at::Tensor s = c.out_whole(a[kResidualIn + 1], "s", at::kFloat, {n.r.C / 128, n.r.T});
+  const hipStream_t st = c.stream();
+  enqueue("puro_residual_norm_quant", [&] { return puro_residual_norm_quant(&n.r, static_cast<uint8_t*>(ptr(q)), ldq, fptr(s), st); });
+  n.done(a);
+  for (int i : {0, 1}) written(a[kResidualIn + i]);
+  return wrap_all(q, s, n.h_out);
+}
+
+// the above, q, s, qT, sT
+PyObject* residual_norm_quant_dual(PyObject* const* a) {
+  Call c;
+  const ResidualIn n(c, a, true);
+  PyObject* const* o = a + kResidualIn;
+  int64_t ldq, ldqT;
+  const at::Tensor q = c.out_rows(o[0], "q", at::kByte, {n.r.T, n.r.C}, ldq);
+  const at::Tensor s = c.out_whole(o[1], "s", at::kFloat, {n.r.C / 128, n.r.T});
+  const at::Tensor qT = c.out_rows(o[2], "qT", at::kByte, {n.r.C, n.r.T}, ldqT);
+  const at::Tensor sT = c.out_whole(o[3], "sT", at::kFloat, {n.r.T / 128, n.r.C});
+  const hipStream_t st = c.stream();
+  enqueue("puro_residual_norm_quant_dual", [&] {
+    return puro_residual_norm_quant_dual(&n.r, static_cast<uint8_t*>(ptr(q)), ldq, fptr(s), static_cast<uint8_t*>(ptr(qT)), ldqT,
+                                         fptr(sT), st);
+  });
+  n.done(a);
+  for (int i : {0, 1, 2, 3}) written(o[i]);
+  return wrap_all(q, s, qT, sT, n.h_out, n.mean, n.rstd, n.post_mean, n.post_rstd);
+}
+
+// dy, h_out, weight, mean, rstd, x, gate, post_weight, post_mean, post_rstd, dh_out, scale, kind, dh, dx, dweight, dbias,
+// dgate, dpost_weight, with_bias, accumulate, workspace
+PyObject* residual_norm_backward(PyObject* const* a) {
+  Call c;
+  puro_residual_grad r = {};
+  r.kind = norm_kind(a[12]);
+  const bool layer = r.kind == PURO_NORM_LAYER;
+  at::ScalarType xt, wt;
+  r.x_dtype = dtype_code(a[1], "h_out", xt);
+  const at::Tensor h = c.rows(a[1], "h_out", xt, nullptr, r.ldh_out);
+  const Shape shape{h.size(0), h.size(1)}, vec{shape[1]}, stat{shape[0]};
+  r.T = shape[0];
+  r.C = shape[1];
+  r.scale = (float)as_float(a[11], "scale");
+  const at::Tensor dy = c.rows(a[0], "dy", xt, &shape, r.lddy);
+  r.w_dtype = dtype_code(a[2], "weight", wt);
+  const at::Tensor weight = c.whole(a[2], "weight", wt, &vec);
+  at::Tensor gate, post, x, mean, post_mean, post_rstd, dho;
+  if (a[6] != Py_None) gate = c.whole(a[6], "gate", wt, &vec);
+  if (a[7] != Py_None) post = c.whole(a[7], "post_weight", wt, &vec);
+  const bool gated = gate.defined() || post.defined();
+  if (layer)
+    mean = c.whole(a[3], "mean", at::kFloat, &stat);
+  else if (a[3] != Py_None || a[8] != Py_None)
+    value_error("mean: an RMS norm has none");
+  const at::Tensor rstd = c.whole(a[4], "rstd", at::kFloat, &stat);
+  if (post.defined()) {
+    if (layer) post_mean = c.whole(a[8], "post_mean", at::kFloat, &stat);
+    post_rstd = c.whole(a[9], "post_rstd", at::kFloat, &stat);
+  } else if (a[8] != Py_None || a[9] != Py_None) {
+    value_error("post_rstd: without post_weight there is no norm of x");
+  }
+  if (a[5] != Py_None) x = c.rows(a[5], "x", xt, &shape, r.ldx);
+  if (gated && !x.defined()) value_error("x: a gate or a norm of it needs the block's output");
+  if (a[10] != Py_None) dho = c.rows(a[10], "dh_out", xt, &shape, r.lddh_out);
+  const bool with_bias = as_bool(a[19]) || a[16] != Py_None, accumulate = as_bool(a[20]);
+  if (a[17] != Py_None && !gate.defined()) value_error("dgate: there is no gate");
+  if (a[18] != Py_None && !post.defined()) value_error("dpost_weight: there is no post_weight");
+  if (accumulate && (a[15] == Py_None || (with_bias && a[16] == Py_None) || (gate.defined() && a[17] == Py_None) ||
+                     (post.defined() && a[18] == Py_None)))
+    value_error("accumulate: needs the gradients it adds to");
+  const at::Tensor dh = c.out_rows(a[13], "dh", xt, shape, r.lddh);
+  at::Tensor dx, db, dg, dp;
+  // (without gate, norm and scale it is dh's equal: dh stands for it)
+  const bool own_dx = gated || r.scale != 1.f || a[14] != Py_None;
+  if (own_dx) dx = c.out_rows(a[14], "dx", xt, shape, r.lddx);
+  const at::Tensor dw = c.out_whole(a[15], "dweight", at::kFloat, vec);
+  if (with_bias) db = c.out_whole(a[16], "dbias", at::kFloat, vec);
+  if (gate.defined()) dg = c.out_whole(a[17], "dgate", at::kFloat, vec);
+  if (post.defined()) dp = c.out_whole(a[18], "dpost_weight", at::kFloat, vec);
+  size_t bytes;
+  const at::Tensor ws = c.workspace(a[21], puro_residual_norm_backward_workspace_size(r.T, r.C, gated ? 1 : 0), bytes);
+  r.dy = ptr(dy);
+  r.h_out = ptr(h);
+  r.dh_out = ptr(dho);
+  r.x = gated ? ptr(x) : nullptr;
+  r.weight = ptr(weight);
+  r.gate = ptr(gate);
+  r.post_weight = ptr(post);
+  r.mean = fptr(mean);
+  r.rstd = fptr(rstd);
+  r.post_mean = fptr(post_mean);
+  r.post_rstd = fptr(post_rstd);
+  r.dh = ptr(dh);
+  r.dx = ptr(dx);
+  r.dweight = fptr(dw);
+  r.dbias = fptr(db);
+  r.dgate = fptr(dg);
+  r.dpost_weight = fptr(dp);
+  r.accumulate = accumulate ? 1 : 0;
+  const hipStream_t st = c.stream();
+  enqueue("puro_residual_norm_backward", [&] { return puro_residual_norm_backward(&r, ptr(ws), bytes, st); });
+  for (int i = 13; i <= 18; ++i) written(a[i]);
+  return wrap_all(dh, own_dx ? dx : dh, dw, db, dg, dp);
+}
+
+// ---- rotary positions --------------------------------------------------------------------------------
+
+// [T, H, D] with unit stride in its heads; the strides of tokens and heads (natural ones where they say nothing).
+const at::Tensor& heads(const Call& c, PyObject* o, const char* what, at::ScalarType dtype, const Shape* shape, int64_t& ld_t,
+                        int64_t& ld_h) {
+  if (!THPVariable_Check(o) || THPVariable_Unpack(o).dim() != 3) value_error(std::string(what) + ": expected a 3-D tensor");
+  const at::Tensor& t = c.tensor(o, what, dtype, shape);
+  if (t.stride(2) != 1 && t.size(2) > 1 && t.numel() > 0)
+    value_error(std::string(what) + ": heads must have unit element stride (got strides " + text(t.strides()) + ")");
+  ld_h = t.size(1) > 1 ? t.stride(1) : t.size(2);
+  ld_t = t.size(0) > 1 ? t.stride(0) : t.size(1) * ld_h;
+  return t;
+}
+
+// x, freqs, positions, start, layout, scale, inverse, y
+PyObject* rotary(PyObject* const* a) {
+  Call c;
+  at::ScalarType xt;
+  int64_t ld_t, ld_h, ldy_t, ldy_h;
+  const int xd = dtype_code(a[0], "x", xt);
+  const at::Tensor x = heads(c, a[0], "x", xt, nullptr, ld_t, ld_h);
+  const Shape shape = x.sizes().vec(), tokens{shape[0]};
+  const at::Tensor freqs = c.whole(a[1], "freqs", at::kDouble, nullptr);
+  if (freqs.dim() != 1 || 2 * freqs.numel() > shape[2])
+    value_error("freqs: expected one value for each pair of at most " + std::to_string(shape[2]) + " columns, got shape " +
+                text(freqs.sizes()));
+  at::Tensor positions;
+  if (a[2] != Py_None) positions = c.whole(a[2], "positions", at::kLong, &tokens);
+  const int64_t start = as_int(a[3], "start"), layout = as_int(a[4], "layout");
+  if (layout != PURO_ROTARY_HALF && layout != PURO_ROTARY_INTERLEAVED)
+    value_error("layout " + std::to_string(layout) + ": expected ROTARY_HALF or ROTARY_INTERLEAVED");
+  const float scale = (float)as_float(a[5], "scale");
+  const bool inverse = as_bool(a[6]);
+  at::Tensor y;
+  if (a[7] != Py_None) {
+    y = heads(c, a[7], "y", xt, &shape, ldy_t, ldy_h);
+  } else {
+    y = c.make(shape, xt);
+    ldy_h = shape[2];
+    ldy_t = shape[1] * shape[2];
+  }
+  const hipStream_t st = c.stream();
+  enqueue("puro_rotary", [&] {
+    return puro_rotary(xd, (int)layout, inverse ? 1 : 0, ptr(x), ld_t, ld_h, shape[0], shape[1], shape[2],
+                       static_cast<const int64_t*>(ptr(positions)), start, static_cast<const double*>(ptr(freqs)), freqs.numel(),
+                       scale, ptr(y), ldy_t, ldy_h, st);
+  });
+  written(a[7]);
+  return wrap(y);
+}
+
+// ---- AdamW -------------------------------------------------------------------------------------------
+
+// A list of `n` tensors (None: there is none).
+bool list_of(PyObject* o, const char* what, Py_ssize_t n) {
+  if (o == Py_None) return false;
+  if (!PyList_Check(o) && !PyTuple_Check(o)) type_error(std::string(what) + ": expected a list of tensors");
+  if (n >= 0 && PySequence_Fast_GET_SIZE(o) != n)
+    value_error(std::string(what) + ": " + std::to_string(PySequence_Fast_GET_SIZE(o)) + " tensors for " + std::to_string(n) +
+                " parameters");
+  return true;
+}
+
+// A number, or a tensor of one value on the GPU (then `dev` points to it).
+template <typename T>
+const T* scalar_tensor(const Call& c, PyObject* o, const char* what, at::ScalarType dtype) {
+  if (!THPVariable_Check(o)) return nullptr;
+  const at::Tensor& t = c.whole(o, what, dtype, nullptr);
+  if (t.numel() != 1) value_error(std::string(what) + ": expected one value");
+  return static_cast<const T*>(t.data_ptr());
+}
+
+// params, grads, exp_avg, exp_avg_sq, step, lr, beta1, beta2, eps, weight_decay, masters, avg_scales, sq_scales, norm,
+// max_norm, seed
+PyObject* adamw(PyObject* const* a) {
+  Call c;
+  if (!list_of(a[0], "params", -1)) type_error("params: expected a list of tensors");
+  const Py_ssize_t n = PySequence_Fast_GET_SIZE(a[0]);
+  const char* names[] = {"params", "grads", "exp_avg", "exp_avg_sq"};
+  for (int i = 1; i < 4; ++i)
+    if (!list_of(a[i], names[i], n)) type_error(std::string(names[i]) + ": expected a list of tensors");
+  const bool masters = list_of(a[10], "masters", n);
+  const bool eight = list_of(a[11], "avg_scales", n);
+  if (list_of(a[12], "sq_scales", n) != eight) value_error("avg_scales and sq_scales: both, or neither");
+  std::vector<puro_adamw_job> jobs((size_t)n);
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    const auto item = [&](int list) { return PySequence_Fast_GET_ITEM(a[list], i); };
+    const auto name = [i](const char* list) { return std::string(list) + "[" + std::to_string(i) + "]"; };
+    puro_adamw_job& j = jobs[(size_t)i];
+    at::ScalarType pt, gt;
+    j.param_dtype = dtype_code(item(0), name("params"), pt);
+    const at::Tensor& p = c.tensor(item(0), name("params"), pt, nullptr);
+    const bool whole = p.is_contiguous();
+    if (!whole && !p.is_non_overlapping_and_dense()) value_error(name("params") + ": must be contiguous");
+    const Shape shape = p.sizes().vec(), blocks{(p.numel() + 127) / 128};
+    // one that goes with it, element by element in memory
+    const auto same = [&](int list, const char* what, at::ScalarType dtype) {
+      const at::Tensor& t = c.tensor(item(list), name(what), dtype, &shape);
+      if (whole ? !t.is_contiguous() : t.strides() != p.strides()) value_error(name(what) + ": must have the parameter's layout");
+      return t.data_ptr();
+    };
+    j.param = p.data_ptr();
+    j.n = p.numel();
+    j.grad_dtype = dtype_code(item(1), name("grads"), gt);
+    j.grad = same(1, "grads", gt);
+    bool codes = false;
+    if (eight) {
+      codes = PySequence_Fast_GET_ITEM(a[11], i) != Py_None;
+      if (codes != (PySequence_Fast_GET_ITEM(a[12], i) != Py_None)) value_error(name("sq_scales") + ": both scales, or neither");
+    }
+    j.exp_avg = same(2, "exp_avg", codes ? at::kByte : at::kFloat);
+    j.exp_avg_sq = same(3, "exp_avg_sq", codes ? at::kByte : at::kFloat);
+    if (codes) {
+      j.avg_scale = fptr(c.whole(item(11), name("avg_scales"), at::kFloat, &blocks));
+      j.sq_scale = fptr(c.whole(item(12), name("sq_scales"), at::kFloat, &blocks));
+    }
+    if (masters && item(10) != Py_None) {
+      if (pt != at::kBFloat16) value_error(name("masters") + ": an fp32 parameter is its own");
+      j.master = static_cast<float*>(same(10, "masters", at::kFloat));
+    }
+  }
+  puro_adamw_hyper h = {};
+  h.step_dev = scalar_tensor<int64_t>(c, a[4], "step", at::kLong);
+  if (!h.step_dev) h.step = as_int(a[4], "step");
+  h.lr_dev = scalar_tensor<float>(c, a[5], "lr", at::kFloat);
+  if (!h.lr_dev) h.lr = as_float(a[5], "lr");
+  h.beta1 = as_float(a[6], "beta1");
+  h.beta2 = as_float(a[7], "beta2");
+  h.eps = as_float(a[8], "eps");
+  h.weight_decay = as_float(a[9], "weight_decay");
+  at::Tensor norm;
+  if (a[13] != Py_None) norm = norm_value(c, a[13]);
+  h.norm = fptr(norm);
+  h.max_norm = (float)as_float(a[14], "max_norm");
+  h.seed = PyLong_Check(a[15]) ? PyLong_AsUnsignedLongLong(a[15]) : 0;
+  if (!PyLong_Check(a[15])) type_error("seed: expected an integer");
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    value_error("seed: expected an integer of 0 to 2^64 - 1");
+  }
+  const hipStream_t st = c.stream();
+  enqueue("puro_adamw", [&] { return puro_adamw(jobs.data(), (int)n, &h, st); });
+  for (int list : {0, 2, 3, 10, 11, 12})
+    if (a[list] != Py_None)
+      for (Py_ssize_t i = 0; i < n; ++i) written(PySequence_Fast_GET_ITEM(a[list], i));
+  Py_RETURN_NONE;
+}
+
 // tensors: for the forward pass of a step that is being captured into a graph (the current stream records).  A leaf's
 // gradient belongs to the stream that was current when the first graph that reaches it was built, for as long as one of
 // those graphs lives, and the autograd engine joins that stream to the backward pass.  One that does not record breaks
@@ -557,6 +886,12 @@ PyMethodDef methods[] = {
     PURO_ENTRY(clip_grad_norm, 5),
     PURO_ENTRY(scale_by_norm, 4),
     PURO_ENTRY(gemm_rows, 7),
+    PURO_ENTRY(residual_norm, 16),
+    PURO_ENTRY(residual_norm_quant, 16),
+    PURO_ENTRY(residual_norm_quant_dual, 18),
+    PURO_ENTRY(residual_norm_backward, 22),
+    PURO_ENTRY(rotary, 8),
+    PURO_ENTRY(adamw, 16),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "Argument marshalling of the operators of puro_ops.h.", -1, methods,

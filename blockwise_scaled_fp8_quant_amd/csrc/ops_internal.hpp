@@ -38,6 +38,8 @@ struct NormArgs {
 hipError_t launch_norm(NormArgs a, hipStream_t st);
 hipError_t launch_norm_quant(NormArgs a, hipStream_t st);
 hipError_t launch_norm_quant_dual(NormArgs a, hipStream_t st);
+// Its second launch alone: the codes of both orientations from x and the statistics in mean and rstd.
+hipError_t launch_norm_tiles(NormArgs a, hipStream_t st);
 
 struct NormBwdArgs {
   const void* dy;
@@ -61,6 +63,104 @@ struct NormBwdArgs {
 // Workgroups of the backward pass: one partial sum of the weight's and bias's gradient each.
 int norm_bwd_blocks(int64_t T, int64_t C);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t st);
+
+// ---- residual sum and norm (residual.hip) -----------------------------------------------------------
+struct ResidualArgs {
+  NormArgs n;              // x: the sum as written (h_out), ldx its row stride; the norm of it, and its outputs
+  const void* h;
+  int64_t ldh;
+  const void* b;           // the block's output
+  int64_t ldb;
+  void* h_out;             // n.x
+  const void* gate;        // optional
+  const void* post;        // weight of the norm of b, optional
+  float scale;
+  float* post_mean;        // optional
+  float* post_rstd;        // optional
+};
+hipError_t launch_residual(ResidualArgs a, hipStream_t st);
+hipError_t launch_residual_quant(ResidualArgs a, hipStream_t st);
+hipError_t launch_residual_quant_dual(ResidualArgs a, hipStream_t st);
+
+struct ResidualBwdArgs {
+  const void* dy;
+  int64_t lddy;
+  const void* h;           // the sum as written
+  int64_t ldh;
+  const void* dho;         // its gradient from behind, optional
+  int64_t lddho;
+  const void* b;           // the block's output (with a gate or a norm of it)
+  int64_t ldb;
+  int64_t T;
+  int C;
+  const void* gamma;
+  const void* gate;        // optional
+  const void* post;        // optional
+  float scale;
+  bool x_bf16, w_bf16;
+  bool layer;
+  const float* mean;
+  const float* rstd;
+  const float* post_mean;
+  const float* post_rstd;
+  void* dh;
+  int64_t lddh;
+  void* dx;                // optional without gate and post
+  int64_t lddx;
+  float* dgamma;
+  float* dbeta;            // optional
+  float* dgate;            // with a gate
+  float* dpost;            // with post
+  int accumulate;
+  float* partial;          // [blocks][2 or 3][C], the workspace
+};
+// Workgroups of the backward pass, and the fp32 vectors of C columns that each leaves in the workspace.
+int residual_bwd_blocks(int64_t T, int64_t C, bool gated);
+constexpr int residual_bwd_sums(bool gated) { return gated ? 3 : 2; }
+hipError_t launch_residual_bwd(const ResidualBwdArgs& a, hipStream_t st);
+
+// ---- rotary positions (rotary.hip) ------------------------------------------------------------------
+constexpr int64_t kRotaryMaxPairs = 2048;   // of a head: its cosines and sines are held in LDS
+
+struct RotaryArgs {
+  const void* x;
+  int64_t ldt, ldh;
+  void* y;
+  int64_t ldyt, ldyh;
+  int64_t T;
+  int H, D, pairs;
+  const double* freqs;
+  const int64_t* positions;   // optional: start + t
+  int64_t start;
+  float scale;
+  bool bf16, interleaved, inverse;
+};
+hipError_t launch_rotary(const RotaryArgs& a, hipStream_t st);
+
+// ---- AdamW (adamw.hip) ------------------------------------------------------------------------------
+struct AdamJob {
+  void* param;
+  float* master;          // optional, of a bf16 param
+  const void* grad;
+  void* avg;
+  void* sq;
+  float* avg_scale;       // of 8-bit states
+  float* sq_scale;
+  int64_t n;
+  uint32_t place;         // in the caller's list
+  bool param_bf16, grad_bf16;
+};
+struct AdamHyper {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  const float* lr_dev;          // optional, in place of lr
+  const int64_t* step_dev;      // optional, in place of step
+  const float* norm;            // optional
+  float max_norm;
+  uint64_t seed;
+};
+// Jobs of 32-bit states, or (eight) of 8-bit ones.
+hipError_t launch_adamw(const AdamJob* jobs, int n_jobs, bool eight, const AdamHyper& h, hipStream_t st);
 
 // ---- gradient norm and clipping (clip.hip) ----------------------------------------------------------
 struct GradJob {

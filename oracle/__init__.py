@@ -37,7 +37,10 @@ Pins (checked by the ``-m "not gpu"`` tests, against things other than this code
                       saturation distance); scaled small integers are exact; the
                       GEMM against pure-Python triple loops and, with unit scales,
                       the plain FP8 matmul.
+  adamw.*             the AdamW step's 8-bit states: random words against Python's integers,
+                      the rounding against the two neighbouring codes and its mean, the decay
+                      that nearest rounding would freeze.
 Parity unpinned: agreement with Puro's own training numerics (their scale
 format, their MXFP8 path) -- the pages print no code, values or error figures.
 """
-from . import e4m3, gemm, mx, quant  # noqa: F401
+from . import adamw, e4m3, gemm, mx, quant  # noqa: F401
