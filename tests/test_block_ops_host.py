@@ -241,3 +241,56 @@ def test_binding_refuses_what_the_library_cannot_see():
         P.puro_adamw([w.half()], [w], [w], [w], 1, 1e-3)
     with pytest.raises(ValueError):
         P.puro_adamw([w], [w, w], [w], [w], 1, 1e-3)
+
+
+def test_rotary_frequencies():
+    """Plain ones by their formula; the scaled ones' ends: the fastest pair is left, the slowest `factor` times slower."""
+    from blockwise_scaled_fp8_quant_amd.rotary import rotary_frequencies
+    plain, one = rotary_frequencies(64, 5000.0)
+    assert one == 1.0 and plain.shape == (32,) and str(plain.dtype) == "torch.float64"
+    for i in (0, 7, 31):
+        assert math.isclose(float(plain[i]), 5000.0 ** (-2 * i / 64), rel_tol=1e-14)
+    linear, one = rotary_frequencies(64, 5000.0, "linear", 4.0)
+    assert one == 1.0 and ((linear * 4 - plain).abs() <= 1e-15 * plain).all()
+    based, one = rotary_frequencies(64, 5000.0, "base", 4.0)
+    assert one == 1.0 and float(based[0]) == 1.0 and math.isclose(float(plain[31] / based[31]), 4.0, rel_tol=1e-12)
+    yarn, scale = rotary_frequencies(64, 5000.0, "yarn", 4.0, trained_length=2048)
+    turns = 2048 * plain / (2 * math.pi)
+    assert math.isclose(scale, 0.1 * math.log(4) + 1)
+    for i in range(32):
+        kept = min(1.0, max(0.0, (float(turns[i]) - 1) / 31))
+        assert math.isclose(float(yarn[i]), float(plain[i]) * (kept + (1 - kept) / 4), rel_tol=1e-12)
+    assert float(yarn[0]) == 1.0 and math.isclose(float(yarn[31]) * 4, float(plain[31]), rel_tol=1e-12)
+    assert rotary_frequencies(64, 5000.0, "yarn", 1.0, trained_length=2048)[1] == 1.0
+    for bad in (dict(columns=7), dict(columns=-2), dict(columns=8, scaling="other"), dict(columns=8, scaling="yarn", factor=2.0),
+                dict(columns=8, scaling="yarn", trained_length=9, low=3.0, high=3.0), dict(columns=8, base=0.0),
+                dict(columns=8, factor=-1.0), dict(columns=2, scaling="base", factor=2.0)):
+        with pytest.raises(ValueError):
+            rotary_frequencies(**bad)
+
+
+def test_captured_steps_are_checked(monkeypatch):
+    """Every differentiable call made while a graph is recorded is checked before its forward pass starts, with every leaf."""
+    import torch
+    from blockwise_scaled_fp8_quant_amd import linear, residual, rotary
+
+    class Stop(Exception):
+        pass
+
+    def check(leaves):
+        raise Stop(sum(isinstance(v, torch.Tensor) for v in leaves))
+    monkeypatch.setattr(linear, "check_capture", check)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+
+    class OnGpu(torch.Tensor):
+        is_cuda = True
+    x = torch.zeros((128, 128), dtype=torch.bfloat16).as_subclass(OnGpu)
+    full = dict(gate=1.0, post_norm=True)
+    freqs, _ = rotary.rotary_frequencies(32)
+    for call, tensors in ((lambda: residual.ResidualNorm(128, **full)(x, x), 6),
+                          (lambda: residual.Fp8ResidualNormLinear(128, 128, **full)(x, x), 7),
+                          (lambda: residual.residual_norm(x, x, x[0]), 3), (lambda: rotary.rotary(x.view(64, 4, 64), freqs), 2),
+                          (lambda: rotary.Rotary(32)(x.view(64, 4, 64)), 2)):
+        with pytest.raises(Stop) as stopped:
+            call()
+        assert stopped.value.args == (tensors,)

@@ -1,0 +1,446 @@
+"""GPU tests of the residual sum, rotary and AdamW modules, and of a training step that runs them together with the layers,
+norms and clipping they stand beside."""
+import copy
+import io
+import math
+
+import pytest
+
+from gpu_util import say, torch
+
+pytestmark = pytest.mark.gpu
+B8 = 2.0 ** -8                   # half a step of bf16
+
+
+@pytest.fixture(scope="module")
+def P():
+    import blockwise_scaled_fp8_quant_amd as P
+    assert torch().cuda.is_available(), "GPU test run without a GPU"
+    return P
+
+
+def bf16(*shape, scale=1.0, seed=0):
+    t = torch()
+    g = t.Generator(device="cuda")
+    g.manual_seed(seed + sum(shape))
+    return (t.randn(shape, generator=g, device="cuda") * scale).bfloat16()
+
+
+@pytest.mark.parametrize("gate,post,scale", [(None, False, 1.0), (0.3, False, 0.5), (None, True, 1.0), (0.3, True, 0.5)])
+@pytest.mark.parametrize("kind", [0, 1])
+def test_residual_module_is_its_entry_points(P, kind, gate, post, scale):
+    """Outputs and gradients are puro_residual_norm's and its backward pass's, bit for bit, with .grad and with main_grad."""
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.residual import ResidualNorm
+    for dtype, main in ((t.bfloat16, False), (t.float32, False), (t.bfloat16, True)):
+        m = ResidualNorm(320, kind, 1e-5, gate, post, scale, dtype=dtype, device="cuda")
+        with t.no_grad():
+            for p in m.parameters():
+                p.add_(t.randn_like(p) * 0.1)
+        if main:
+            m.enable_main_grad()
+        h, x = (bf16(2, 9, 320, seed=k).to(dtype).requires_grad_(True) for k in range(2))
+        dy, dho = (bf16(2, 9, 320, seed=5 + k).to(dtype) for k in range(2))
+        y, h_out = m(h, x)
+        vec = dict(gate=m.gate, post_weight=m.post_weight, scale=scale, kind=kind)
+        h2, x2 = h.detach().view(18, 320), x.detach().view(18, 320)
+        y1, o1, *stats = P.puro_residual_norm(h2, x2, m.weight, m.bias, **vec)
+        assert t.equal(y.view(18, 320), y1) and t.equal(h_out.view(18, 320), o1)
+        for times in (1, 2):                                # the second pass adds to the gradients of the first
+            t.autograd.backward(m(h, x), (dy, dho))
+            want = P.puro_residual_norm_backward(dy.view(18, 320), o1, m.weight, *stats[:2], x=x2, post_mean=stats[2],
+                                                 post_rstd=stats[3], dh_out=dho.view(18, 320), with_bias=kind == 0, **vec)
+            assert h.grad.data_ptr() != x.grad.data_ptr()
+            for got, w in ((h.grad, want[0]), (x.grad, want[1])):
+                assert t.equal(got.view(18, 320), w * times)
+            for p, w in zip((m.weight, m.bias, m.gate, m.post_weight), want[2:]):
+                if p is None:
+                    assert w is None
+                elif main:
+                    assert p.grad is None and t.equal(p.main_grad, w * times)
+                else:
+                    assert t.equal(p.grad, w.to(dtype) * times)
+
+
+def test_residual_module_with_parts_of_its_gradients(P):
+    """One output alone is used; some inputs need no gradient; broadcast gradients; a second backward pass is refused."""
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.residual import ResidualNorm, residual_norm
+    m = ResidualNorm(256, 0, gate=0.5, post_norm=True, dtype=t.float32, device="cuda")
+    h, x = (t.randn((4, 256), device="cuda", requires_grad=True) for _ in range(2))
+    y, h_out = m(h, x)
+    g0 = t.autograd.grad(y.sum() + 0 * h_out.sum(), [h, x, *m.parameters()])
+    y, h_out = m(h, x)
+    g1 = t.autograd.grad(y.sum(), [h, x, *m.parameters()])          # no gradient of h_out
+    assert all(t.equal(a, b) for a, b in zip(g0, g1))
+    y, h_out = m(h, x)
+    g2 = t.autograd.grad(h_out.sum(), [h, x, m.gate, m.post_weight, m.weight, m.bias])   # none of y
+    assert t.equal(g2[0], t.ones_like(h)) and (g2[4] == 0).all() and (g2[5] == 0).all() and g2[2].any()
+    m.weight.requires_grad_(False)
+    m.gate.requires_grad_(False)
+    y, h_out = m(h.detach(), x)
+    y.sum().backward()
+    assert m.weight.grad is None and m.gate.grad is None and m.bias.grad is not None and t.equal(x.grad, g1[1])
+    w = t.ones(256, device="cuda", requires_grad=True)
+    y, h_out = residual_norm(h, x, w, kind=P.RMS_NORM)
+    (g,) = t.autograd.grad(y.sum(), h, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+    with pytest.raises(ValueError):
+        residual_norm(h, x[:3], w)
+    m2 = ResidualNorm(256, 0, gate=0.5, dtype=t.float32, device="cuda")
+    m2.weight.main_grad = t.zeros(256, device="cuda")
+    with pytest.raises(ValueError):
+        m2(h, x)[0].sum().backward()                                 # a main_grad of one vector alone
+    # saved tensors that changed are noticed
+    y, h_out = m(h, x)
+    with t.no_grad():
+        h_out.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
+def test_fp8_residual_norm_linear(P):
+    """(h, x) -> (norm(h + x) W^T, h + x): forward as the sum in bf16 and Fp8NormLinear, bit for bit; backward as the chain of its
+    entry points."""
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.norm import Fp8NormLinear
+    from blockwise_scaled_fp8_quant_amd.residual import Fp8ResidualNormLinear
+    m = Fp8ResidualNormLinear(256, 384, kind=P.RMS_NORM, device="cuda")
+    ref = Fp8NormLinear(256, 384, kind=P.RMS_NORM, device="cuda")
+    with t.no_grad():
+        m.norm.weight.add_(bf16(256, scale=0.1))
+        ref.norm.weight.copy_(m.norm.weight)
+        ref.linear.weight.copy_(m.linear.weight)
+    for mod in (m, ref):
+        mod.enable_main_grad()
+    h, x = (bf16(2, 128, 256, seed=k).requires_grad_(True) for k in range(2))
+    dy, dho = bf16(2, 128, 384, scale=1e-2), bf16(2, 128, 256, scale=1e-2, seed=3)
+    y, h_out = m(h, x)
+    s = (h + x).detach().requires_grad_(True)
+    yr = ref(s)
+    assert t.equal(h_out, s) and t.equal(y, yr)
+    t.autograd.backward((y, h_out), (dy, dho))
+    yr.backward(dy)
+    assert t.equal(m.linear.weight.main_grad, ref.linear.weight.main_grad)
+    # the norm's gradients see the same dN: their sums run in the same order
+    assert t.equal(m.norm.weight.main_grad, ref.norm.weight.main_grad)
+    # here dN's part and dh_out are added before the rounding, there after: a half step of the part, one of the sum on each side
+    want = s.grad.float() + dho.float()
+    off = B8 * (s.grad.float().abs() + want.abs() * 1.01) + 1e-30
+    assert ((h.grad.float() - want).abs() <= off).all() and t.equal(h.grad, x.grad) and h.grad.data_ptr() != x.grad.data_ptr()
+    with pytest.raises(P.PuroError):
+        m(h[:, :100], x[:, :100])                                    # 200 rows with gradients
+    with pytest.raises(ValueError):
+        m(h, x, codes=m.quantize_weight())
+    with t.no_grad():                                                # any number of rows, and a weight's codes that are kept
+        codes = m.quantize_weight()
+        for T in (1, 7, 200):
+            a, o = m(h.view(256, 256)[:T], x.view(256, 256)[:T], codes)
+            b = ref((h + x).view(256, 256)[:T], ref.quantize_weight())
+            assert t.equal(a, b) and t.equal(o, (h + x).view(256, 256)[:T])
+
+
+def test_rotary_module(P):
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.rotary import Rotary, rotary, rotary_frequencies
+    for layout in (P.ROTARY_HALF, P.ROTARY_INTERLEAVED):
+        r = Rotary(32, layout=layout, scaling="yarn", factor=4.0, trained_length=512).to(t.bfloat16).cuda()
+        x = t.randn((2, 20, 3, 48), device="cuda", requires_grad=True)
+        y = r(x, start=5)
+        freqs, scale = rotary_frequencies(32, scaling="yarn", factor=4.0, trained_length=512, device="cuda")
+        for b in range(2):                                           # every sequence counts from the start
+            assert t.equal(y[b], P.puro_rotary(x[b].detach(), freqs, start=5, layout=layout, scale=scale))
+        pos = t.randint(0, 900, (2, 20), device="cuda")
+        z = r(x, pos)
+        assert t.equal(z[1], P.puro_rotary(x[1].detach(), freqs, pos[1], layout=layout, scale=scale))
+        assert t.equal(r(x, pos[0])[1], P.puro_rotary(x[1].detach(), freqs, pos[0], layout=layout, scale=scale))
+        dz = t.randn_like(z)
+        z.backward(dz)
+        assert t.equal(x.grad[0], P.puro_rotary(dz[0], freqs, pos[0], layout=layout, scale=scale, inverse=True))
+        # twice: the turn is linear, so the gradient of (gradient . v) with respect to dz is the turn of v
+        v, w = t.randn_like(x), dz.clone().requires_grad_(True)
+        (g,) = t.autograd.grad(r(x, pos), x, w, create_graph=True)
+        (gw,) = t.autograd.grad(g, w, v)
+        assert t.equal(gw[0], P.puro_rotary(v[0], freqs, pos[0], layout=layout, scale=scale))
+        # a broadcast gradient, and part of wider rows
+        r(x, pos).sum().backward()
+        wide = t.randn((20, 5, 48), device="cuda")
+        assert t.equal(r(wide[:, 1:4]), P.puro_rotary(wide[:, 1:4].contiguous(), freqs, layout=layout, scale=scale))
+    with pytest.raises(ValueError):
+        rotary(x[0, 0], freqs)
+    with pytest.raises(ValueError):
+        rotary(x, freqs, pos[:, :3])
+    for bad in (dict(columns=3), dict(columns=0), dict(columns=8, scaling="cubic"), dict(columns=8, scaling="yarn"),
+                dict(columns=8, factor=0.0), dict(columns=2, scaling="base")):
+        with pytest.raises(ValueError):
+            rotary_frequencies(**bad)
+
+
+def reference_adamw(params, grads, lr, betas, eps, decay, step, m, v):
+    """One step in 64 bits, in place."""
+    for p, g, a, b in zip(params, grads, m, v):
+        a.mul_(betas[0]).add_(g, alpha=1 - betas[0])
+        b.mul_(betas[1]).addcmul_(g, g, value=1 - betas[1])
+        p.mul_(1 - lr * decay).sub_(lr / (1 - betas[0] ** step) * a / ((b / (1 - betas[1] ** step)).sqrt() + eps))
+
+
+def test_adamw_class(P):
+    """Ten steps over groups with their own options, gradients in .grad and main_grad, in several layouts, a parameter that joins
+    late; against 64 bits.  A step adds at most 30 roundings of fp32 to an update of at most lr / (1 - beta1) in size
+    and 3 to the parameter."""
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.adamw import AdamW
+    from blockwise_scaled_fp8_quant_amd.linear import Fp8Linear
+    U = 2.0 ** -24
+    lin = Fp8Linear(256, 128, device="cuda")
+    lin.enable_main_grad()
+    a = t.nn.Parameter(t.randn((30, 7), device="cuda"))
+    b = t.nn.Parameter(t.randn((9, 5), device="cuda").t())
+    late = t.nn.Parameter(t.randn(11, device="cuda"))
+    opt = AdamW([{"params": [lin.weight, a]}, {"params": [b, late], "weight_decay": 0.0, "lr": 1e-2, "betas": (0.8, 0.99)}],
+                lr=1e-3, weight_decay=0.1)
+    held = [p.detach().double() for p in (lin.weight, a, b, late)]
+    m, v = [t.zeros_like(p) for p in held], [t.zeros_like(p) for p in held]
+    for k in range(1, 11):
+        opt.zero_grad()
+        assert a.grad is None and (lin.weight.main_grad == 0).all()
+        g = [t.randn_like(p).float() * 1e-2 for p in held]
+        lin.weight.main_grad.copy_(g[0])
+        a.grad, b.grad = g[1], (g[2].contiguous() if k % 2 else g[2])
+        late.grad = g[3] if k > 4 else None
+        assert opt.step(lambda: 5.0) == 5.0
+        reference_adamw(held[:2], [x.double() for x in g[:2]], 1e-3, (0.9, 0.999), 1e-8, 0.1, k, m[:2], v[:2])
+        reference_adamw(held[2:3], [g[2].double()], 1e-2, (0.8, 0.99), 1e-8, 0.0, k, m[2:3], v[2:3])
+        if k > 4:
+            reference_adamw(held[3:], [g[3].double()], 1e-2, (0.8, 0.99), 1e-8, 0.0, k - 4, m[3:], v[3:])
+    for p, h, lr in zip((opt.state[lin.weight]["master"], a, b, late), held, (1e-3, 1e-3, 1e-2, 1e-2)):
+        assert ((p.detach().double() - h).abs() <= 10 * U * (30 * 10 * lr + 3 * h.abs() + 3 * 10 * lr)).all()
+    assert t.equal(lin.weight, opt.state[lin.weight]["master"].bfloat16())
+    assert opt.state[late]["step"] == 6 and opt.state[a]["step"] == 10
+    with t.no_grad():
+        lin.weight.fill_(1.0)
+    opt.sync_masters()
+    assert (opt.state[lin.weight]["master"] == 1).all()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_saves_and_loads(P, bits):
+    """A run that is saved and continued by another optimizer, or by a copy, gives the same bits."""
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.adamw import AdamW
+
+    def model():
+        t.manual_seed(3)
+        return [t.nn.Parameter(t.randn(1000, device="cuda").bfloat16()), t.nn.Parameter(t.randn((20, 30), device="cuda"))]
+
+    def run(opt, params, steps):
+        for k in steps:
+            for i, p in enumerate(params):
+                p.grad = bf16(*p.shape, scale=1e-2, seed=100 * k + i).to(p.dtype)
+            opt.step(max_norm=0.1)
+    one = model()
+    opt = AdamW(one, lr=1e-3, state_bits=bits, seed=9)
+    run(opt, one, range(5))
+    file = io.BytesIO()
+    t.save(opt.state_dict(), file)
+    file.seek(0)
+    two = model()
+    with t.no_grad():
+        for p, q in zip(two, one):
+            p.copy_(q)
+    other = AdamW(two, lr=77.0, state_bits=40 - bits)                 # the saved options replace these
+    other.load_state_dict(t.load(file, weights_only=True))
+    both = copy.deepcopy((opt, one))
+    run(opt, one, range(5, 9))
+    run(other, two, range(5, 9))
+    run(*both, range(5, 9))
+    for p, q, r in zip(one, two, both[1]):
+        assert t.equal(p, q) and t.equal(p, r)
+        for name, x in opt.state[p].items():
+            y, z = other.state[q][name], both[0].state[r][name]
+            assert (x == y == z) if name == "step" else x.dtype == y.dtype and t.equal(x, y) and t.equal(x, z)
+    assert opt.state[one[0]]["exp_avg"].dtype == (t.uint8 if bits == 8 else t.float32)
+
+
+def test_adamw_refusals(P):
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.adamw import AdamW
+    p = t.nn.Parameter(t.zeros(4, device="cuda"))
+    for bad in (dict(state_bits=16), dict(state_bits=None)):
+        with pytest.raises(ValueError):
+            AdamW([p], **bad)
+    p.grad = t.zeros(4, device="cuda")
+    with pytest.raises(P.PuroError):
+        AdamW([p], betas=(1.0, 0.9)).step()
+    opt = AdamW([p], lr=float("nan"))
+    with pytest.raises(P.PuroError):
+        opt.step()
+    assert opt.state[p]["step"] == 0                                  # a refused step is none
+    half = t.nn.Parameter(t.zeros(4, device="cuda").half())
+    half.grad = t.zeros_like(half)
+    with pytest.raises(TypeError):
+        AdamW([half]).step()
+    host = t.nn.Parameter(t.zeros(4))
+    host.grad = t.zeros(4)
+    with pytest.raises(ValueError):
+        AdamW([host]).step()
+    q = t.nn.Parameter(t.zeros(4, device="cuda"))
+    with pytest.raises(RuntimeError, match="every parameter"):
+        AdamW([p, q], capturable=True).step()
+    plain, fresh = AdamW([p]), AdamW([p], capturable=True)
+    plain.step()
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        for opt in (plain, fresh):
+            with pytest.raises(RuntimeError, match="being captured"):
+                opt.step()
+        y = p.detach() + 1
+    graph.replay()
+    t.cuda.synchronize()
+    assert (y == 1).all()
+
+
+def make_block(P, kind, state_bits=32, capturable=False):
+    """Two blocks of a small decoder: norm + qkv, rotary, a stand-in for the attention, o, residual + norm + gate/up, gated
+    activation, down, and the residual + norm at the end."""
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.adamw import AdamW
+    from blockwise_scaled_fp8_quant_amd.linear import Fp8Linear
+    from blockwise_scaled_fp8_quant_amd.norm import Fp8NormLinear
+    from blockwise_scaled_fp8_quant_amd.residual import Fp8ResidualNormLinear, ResidualNorm
+    from blockwise_scaled_fp8_quant_amd.rotary import Rotary
+    t.manual_seed(11)
+
+    class Model(t.nn.Module):
+        def __init__(self):
+            super().__init__()
+            dev = dict(device="cuda")
+            self.first = Fp8NormLinear(256, 512, kind=kind, **dev)                       # 4 query, 2 key, 2 value heads of 64
+            self.rotary = Rotary(64)
+            self.o = t.nn.ModuleList([Fp8Linear(256, 256, **dev) for _ in range(2)])
+            self.up = t.nn.ModuleList([Fp8ResidualNormLinear(256, 512, kind, gate=0.5, post_norm=True, **dev),
+                                       Fp8ResidualNormLinear(256, 512, kind, **dev)])
+            self.down = t.nn.ModuleList([Fp8Linear(256, 256, **dev) for _ in range(2)])
+            self.qkv = Fp8ResidualNormLinear(256, 512, kind, scale=0.7, **dev)
+            self.last = ResidualNorm(256, kind, **dev)
+
+        def attend(self, qkv):
+            heads = qkv.view(-1, 8, 64)
+            turned = self.rotary(heads[:, :6])
+            q, k, v = turned[:, :4].float(), turned[:, 4:].float(), heads[:, 6:].float()
+            score = (q * k.repeat_interleave(2, 1)).sum(-1, keepdim=True) / 8
+            return (score.sigmoid() * v.repeat_interleave(2, 1)).bfloat16().reshape(-1, 256)
+
+        def mlp(self, u):
+            gate, up = u.float().chunk(2, -1)
+            return (t.nn.functional.silu(gate) * up).bfloat16()
+
+        def forward(self, h):
+            qkv = self.first(h)
+            for i in range(2):
+                u, h = self.up[i](h, self.o[i](self.attend(qkv)))
+                x = self.down[i](self.mlp(u))
+                if i == 0:
+                    qkv, h = self.qkv(h, x)
+            return self.last(h, x)
+    m = Model()
+    for mod in (m.first, m.qkv, m.last, *m.o, *m.up, *m.down):
+        mod.enable_main_grad()
+    return m, AdamW(m.parameters(), lr=1e-3, state_bits=state_bits, capturable=capturable, seed=1)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("kind", [1, 0])
+def test_training_step(P, kind, bits):
+    """Forward, backward, clipping and the step of two blocks: every parameter has a finite gradient and moves, the step is
+    puro_adamw's on what the backward pass left, and micro-batches add up."""
+    t = torch()
+    m, opt = make_block(P, kind, bits)
+    x, dy = bf16(256, 256), bf16(256, 256, scale=1e-2, seed=4)
+    for step in range(1, 4):
+        opt.zero_grad()
+        y, h = m(x)
+        t.autograd.backward((y, h), (dy, dy))
+        once = {k: p.main_grad.clone() for k, p in m.named_parameters()}
+        assert all(g.isfinite().all() and g.any() for g in once.values()), [k for k, g in once.items() if not g.any()]
+        y, h = m(x)
+        t.autograd.backward((y, h), (dy, dy))
+        for k, p in m.named_parameters():
+            assert t.allclose(p.main_grad, 2 * once[k], rtol=1e-5, atol=0), k         # (one fp32 addition)
+        copies = copy.deepcopy([(p.detach(), p.main_grad, opt.state.get(p)) for p in m.parameters()])
+        opt.step(max_norm=0.5)
+        grads = [g for _, g, _ in copies]
+        norm = P.puro_grad_norm(grads)
+        assert t.equal(norm, opt.grad_norm)
+        if step > 1:
+            get = lambda name: [s[name] for _, _, s in copies] if name in copies[0][2] else None
+            P.puro_adamw([p for p, _, _ in copies], grads, get("exp_avg"), get("exp_avg_sq"), step, 1e-3, masters=get("master"),
+                         avg_scales=get("avg_scale"), sq_scales=get("sq_scale"), norm=norm, max_norm=0.5, seed=1)
+            for (p, _, s), q in zip(copies, m.parameters()):
+                assert t.equal(p, q) and t.equal(s["exp_avg"], opt.state[q]["exp_avg"])
+                assert t.equal(s["master"], opt.state[q]["master"]) and t.equal(s["master"].bfloat16(), p)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_training_step_in_a_graph(P, bits):
+    """The whole step captured; every replay, with other inputs and eager work in between, gives the eager step's bits."""
+    t = torch()
+    (m, opt), (e, eopt) = (make_block(P, 1, bits, capturable=c) for c in (True, False))
+    for p, q in zip(m.parameters(), e.parameters()):
+        assert t.equal(p, q)
+    xin, dyin = bf16(128, 256), bf16(128, 256, scale=1e-2, seed=4)
+
+    def step(mod, o, x, dy):
+        o.zero_grad()
+        y, h = mod(x)
+        t.autograd.backward((y, h), (dy, dy))
+        o.step(max_norm=0.5)
+        return y.detach()
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        step(m, opt, xin, dyin)
+    t.cuda.current_stream().wait_stream(side)
+    step(e, eopt, xin, dyin)
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        y = step(m, opt, xin, dyin)
+    x0, dy0 = xin.clone(), dyin.clone()
+    for k in range(3):
+        xin.copy_(x0 * (k + 1) - k)
+        dyin.copy_(dy0 / (k + 1))
+        graph.replay()
+        t.cuda.synchronize()
+        assert t.equal(y, step(e, eopt, xin, dyin)), k
+        for (name, p), q in zip(m.named_parameters(), e.parameters()):
+            assert t.equal(p, q) and t.equal(p.main_grad, q.main_grad), (k, name)
+            assert t.equal(opt.state[p]["exp_avg_sq"], eopt.state[q]["exp_avg_sq"]), (k, name)
+    assert int(next(iter(opt.state.values()))["step"]) == 4
+
+
+def test_capture_over_a_living_graph_is_refused(P):
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.residual import Fp8ResidualNormLinear, ResidualNorm
+    from blockwise_scaled_fp8_quant_amd.rotary import rotary, rotary_frequencies
+    h = bf16(128, 256).requires_grad_(True)
+    x = bf16(128, 256, seed=1)
+    m, n = Fp8ResidualNormLinear(256, 256, gate=0.1, device="cuda"), ResidualNorm(256, gate=0.1, device="cuda")
+    freqs, _ = rotary_frequencies(32, device="cuda")
+    heads = h.view(128, 8, 32)
+    living = [m(h, x), n(h, x), rotary(heads, freqs)]
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        for call in (lambda: m(h, x), lambda: n(x, h), lambda: m(x, x), lambda: n(x, x), lambda: rotary(h.view(128, 8, 32), freqs)):
+            with pytest.raises(RuntimeError, match="captured"):
+                call()
+        with t.no_grad():
+            y, _ = m(h, x)
+    graph.replay()
+    t.cuda.synchronize()
+    say("[block] capture refused")
+    with t.no_grad():
+        assert t.equal(y, m(h, x)[0])
+    for v in living:
+        (v if isinstance(v, t.Tensor) else v[0] + 0 * v[1].sum()).backward(t.ones_like(v if isinstance(v, t.Tensor) else v[0]))
+    assert h.grad.isfinite().all() and math.isfinite(float(m.norm.gate.grad.sum()))
