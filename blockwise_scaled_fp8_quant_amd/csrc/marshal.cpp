@@ -137,6 +137,13 @@ class Call {
     return t;
   }
 
+  // Whether an object is a tensor that `tensor` and `whole` would take (of `dtype`, where it is named), at less cost.
+  bool plain(PyObject* o, at::ScalarType dtype) const {
+    if (!THPVariable_Check(o)) return false;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    return t.is_cuda() && t.get_device() == dev_ && t.layout() == at::kStrided && t.scalar_type() == dtype;
+  }
+
   at::Tensor make(const Shape& shape, at::ScalarType dtype) const {
     // torch.empty without its dispatch, which costs as much as the allocation
     return at::Tensor(at::detail::empty_cuda(shape, dtype, at::Device(at::kCUDA, (c10::DeviceIndex)dev_), c10::nullopt));
@@ -769,33 +776,51 @@ PyObject* adamw(PyObject* const* a) {
   for (Py_ssize_t i = 0; i < n; ++i) {
     const auto item = [&](int list) { return PySequence_Fast_GET_ITEM(a[list], i); };
     const auto name = [i](const char* list) { return std::string(list) + "[" + std::to_string(i) + "]"; };
+    // (names are made for errors alone: a list has hundreds of tensors)
+    const auto type_of = [&](int list, const char* what, at::ScalarType& st) {
+      if (THPVariable_Check(item(list))) {
+        st = THPVariable_Unpack(item(list)).scalar_type();
+        if (st == at::kBFloat16) return (int)PURO_OUT_BF16;
+        if (st == at::kFloat) return (int)PURO_OUT_FP32;
+      }
+      return dtype_code(item(list), name(what), st);
+    };
+    const auto take = [&](int list, const char* what, at::ScalarType dtype) -> const at::Tensor& {
+      return c.plain(item(list), dtype) ? THPVariable_Unpack(item(list)) : c.tensor(item(list), name(what), dtype, nullptr);
+    };
     puro_adamw_job& j = jobs[(size_t)i];
     at::ScalarType pt, gt;
-    j.param_dtype = dtype_code(item(0), name("params"), pt);
-    const at::Tensor& p = c.tensor(item(0), name("params"), pt, nullptr);
+    j.param_dtype = type_of(0, "params", pt);
+    const at::Tensor& p = take(0, "params", pt);
     const bool whole = p.is_contiguous();
     if (!whole && !p.is_non_overlapping_and_dense()) value_error(name("params") + ": must be contiguous");
-    const Shape shape = p.sizes().vec(), blocks{(p.numel() + 127) / 128};
     // one that goes with it, element by element in memory
     const auto same = [&](int list, const char* what, at::ScalarType dtype) {
-      const at::Tensor& t = c.tensor(item(list), name(what), dtype, &shape);
+      const at::Tensor& t = take(list, what, dtype);
+      if (t.sizes() != p.sizes()) value_error(name(what) + ": shape " + text(t.sizes()) + ", expected " + text(p.sizes()));
       if (whole ? !t.is_contiguous() : t.strides() != p.strides()) value_error(name(what) + ": must have the parameter's layout");
       return t.data_ptr();
     };
     j.param = p.data_ptr();
     j.n = p.numel();
-    j.grad_dtype = dtype_code(item(1), name("grads"), gt);
+    j.grad_dtype = type_of(1, "grads", gt);
     j.grad = same(1, "grads", gt);
     bool codes = false;
     if (eight) {
-      codes = PySequence_Fast_GET_ITEM(a[11], i) != Py_None;
-      if (codes != (PySequence_Fast_GET_ITEM(a[12], i) != Py_None)) value_error(name("sq_scales") + ": both scales, or neither");
+      codes = item(11) != Py_None;
+      if (codes != (item(12) != Py_None)) value_error(name("sq_scales") + ": both scales, or neither");
     }
     j.exp_avg = same(2, "exp_avg", codes ? at::kByte : at::kFloat);
     j.exp_avg_sq = same(3, "exp_avg_sq", codes ? at::kByte : at::kFloat);
     if (codes) {
-      j.avg_scale = fptr(c.whole(item(11), name("avg_scales"), at::kFloat, &blocks));
-      j.sq_scale = fptr(c.whole(item(12), name("sq_scales"), at::kFloat, &blocks));
+      const Shape blocks{(j.n + 127) / 128};
+      const auto scale = [&](int list, const char* what) {
+        const at::Tensor& t = take(list, what, at::kFloat);
+        if (t.sizes() != at::IntArrayRef(blocks) || !t.is_contiguous()) return fptr(c.whole(item(list), name(what), at::kFloat, &blocks));
+        return fptr(t);
+      };
+      j.avg_scale = scale(11, "avg_scales");
+      j.sq_scale = scale(12, "sq_scales");
     }
     if (masters && item(10) != Py_None) {
       if (pt != at::kBFloat16) value_error(name("masters") + ": an fp32 parameter is its own");

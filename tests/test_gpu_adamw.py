@@ -284,6 +284,34 @@ def test_eight_bit_states_keep_up_with_the_gradients(P):
     assert float(root.std()) <= 0.18 and abs(float(root.mean()) - 1.001) <= 0.02 + 6 * 0.18 / math.sqrt(n)
 
 
+@pytest.mark.parametrize("exponent", [-149, -126, -100, -60, -49, -48, -47, -30, -1, 20, 40, 62])
+def test_states_of_every_size(P, exponent):
+    """Gradients and states about 2^exponent, of many sizes within a block, zeros among them, down to subnormal numbers and squares
+    that vanish or overflow: 8-bit states as the oracle's, to the bit; a block of one size beside them."""
+    t = torch()
+    n = 128 * 40 + 77
+    s = Set([n], eight=True, seed=exponent & 255)
+    g = t.Generator(device="cuda")
+    g.manual_seed(5)
+    size = t.exp2(exponent + 12 * t.rand(n, generator=g, device="cuda", dtype=t.float64))
+    size[::7] = 0
+    size[1280:1408] = 2.0 ** exponent
+    size[2560:3000] = 0
+    s.grads[0].copy_(size * t.randn(n, generator=g, device="cuda"))
+    for scale, part in ((s.avg_scale[0], 0.1), (s.sq_scale[0], 0.3)):
+        scale.copy_(t.full_like(scale, 1.0).double() * 2.0 ** max(exponent, -140) * part / 448)
+    s.avg[0][2560:3000], s.sq[0][2560:2800] = 0, 0
+    before = s.copies()
+    s.step(P, 3, seed=8)
+    with np.errstate(over="ignore", invalid="ignore"):
+        qa, qr, sa, sr, _, _ = oracle.step8(host(s.grads[0]), *(host(before[k][0]) for k in (2, 3, 4, 5)), HYPER["beta1"],
+                                            HYPER["beta2"], 8, 3, 0)
+    assert np.array_equal(host(s.avg_scale[0]), sa) and np.array_equal(host(s.sq_scale[0]), sr)
+    for got, want in ((host(s.avg[0]), qa), (host(s.sq[0]), qr)):        # (NaN has two codes, and zero's sign is none's)
+        either = np.isin(want & 0x7F, (0, 0x7F))
+        assert np.array_equal(got & 0x7F, want & 0x7F) and np.array_equal(got[~either], want[~either])
+
+
 def test_layouts(P):
     """Matrices dense in another order of their dimensions, with everything that goes with them in the same one."""
     t = torch()
