@@ -27,7 +27,8 @@ MARSHAL = os.path.join(PKG, "_marshal.so")
 ARCH = "gfx950"
 
 SOURCES = ["quant.hip", "gemm.hip", "gemm_w4.hip", "abi.cpp",
-           "norm.hip", "clip.hip", "gemm_rows.hip", "residual.hip", "rotary.hip", "adamw.hip", "abi_ops.cpp"]
+           "norm.hip", "clip.hip", "gemm_rows.hip", "residual.hip", "residual_bwd.hip",
+           "rotary.hip", "adamw.hip", "abi_ops.cpp"]
 
 
 def _hipcc() -> str:

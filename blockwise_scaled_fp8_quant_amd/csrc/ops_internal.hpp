@@ -64,7 +64,10 @@ struct NormBwdArgs {
 int norm_bwd_blocks(int64_t T, int64_t C);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t st);
 
-// ---- residual sum and norm (residual.hip) -----------------------------------------------------------
+// ---- residual sum and norm (residual.hip, residual_bwd.hip) -------------------------------------------
+// Whether a call that moves `passes` times T C elements of es bytes reads past the caches.
+bool beyond_cache(int64_t T, int64_t C, int64_t es, int passes);
+
 struct ResidualArgs {
   NormArgs n;              // x: the sum as written (h_out), ldx its row stride; the norm of it, and its outputs
   const void* h;
@@ -77,6 +80,7 @@ struct ResidualArgs {
   float scale;
   float* post_mean;        // optional
   float* post_rstd;        // optional
+  bool stream;             // filled in by the launcher: h and b are read past the caches
 };
 hipError_t launch_residual(ResidualArgs a, hipStream_t st);
 hipError_t launch_residual_quant(ResidualArgs a, hipStream_t st);
@@ -113,11 +117,12 @@ struct ResidualBwdArgs {
   float* dpost;            // with post
   int accumulate;
   float* partial;          // [blocks][2 or 3][C], the workspace
+  bool stream;             // filled in by the launcher: the rows are read past the caches
 };
 // Workgroups of the backward pass, and the fp32 vectors of C columns that each leaves in the workspace.
 int residual_bwd_blocks(int64_t T, int64_t C, bool gated);
 constexpr int residual_bwd_sums(bool gated) { return gated ? 3 : 2; }
-hipError_t launch_residual_bwd(const ResidualBwdArgs& a, hipStream_t st);
+hipError_t launch_residual_bwd(ResidualBwdArgs a, hipStream_t st);
 
 // ---- rotary positions (rotary.hip) ------------------------------------------------------------------
 constexpr int64_t kRotaryMaxPairs = 2048;   // of a head: its cosines and sines are held in LDS

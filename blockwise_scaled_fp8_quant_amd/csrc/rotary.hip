@@ -14,18 +14,24 @@
 #include "rows.hpp"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace puro {
 
 namespace {
 
 constexpr int kThreads = 256;
+// Chunks of a workgroup's tile.  Measured, us, 16384 x 24 x 128 bf16 half and 8192 x 24 x 128 fp32 interleaved, half of the head:
+// 33.6 (6.0 TB/s) and 32.4 (6.2); 512 chunks 32.3 and 37.0, 256 33.9 and 41.1 (a tile's few tokens have as many angles), 2048
+// 33.7 and 33.0, and 64 tokens of the latter 4.9 in place of 4.2.  Chunks of eight fp32 columns, where a wave's accesses
+// leave gaps, 40.1.
+constexpr int kTileChunks = 1024;
 
 struct RotaryPlan {
   int tokens;        // of a workgroup's tile
   int heads;         // of a workgroup's tile
   int splits;        // tiles that share their tokens
-  int units;         // chunks of a head: eight pairs, or eight columns
+  int units;         // chunks of a head: of 16 bytes, or two of them that make pairs (half layout)
   int turned;        // the first of them hold pairs (half layout), the others copied columns
   int64_t tiles;
 };
@@ -42,15 +48,80 @@ __device__ __forceinline__ float2 cos_sin(double position, double freq, float sc
   return make_float2(scale * co, scale * (inverse ? -si : si));
 }
 
+// 16 bytes of a head: eight bf16 columns or four fp32 ones, nv of them there (a whole chunk where VEC), so that a wave's
+// accesses fill whole lines.
+template <bool BF16>
+constexpr int kPer = BF16 ? 8 : 4;
+
+template <bool BF16, bool VEC, bool NT>
+__device__ __forceinline__ u32x4 load16(const void* base, int64_t at, int nv) {
+  if constexpr (BF16) {
+    return settle8<true, VEC>(load8<true, VEC, NT>(base, at, nv), nv).w[0];
+  } else {
+    const uint32_t* p = static_cast<const uint32_t*>(base) + at;
+    if constexpr (VEC) {
+      const u32x4* v = reinterpret_cast<const u32x4*>(p);
+      if constexpr (NT) return __builtin_nontemporal_load(v);
+      return *v;
+    }
+    if (nv == 4) return *reinterpret_cast<const u32x4_a4*>(p);
+    u32x4 w = {0u, 0u, 0u, 0u};
+    if (nv > 0) w.x = p[0];
+    if (nv > 1) w.y = p[1];
+    if (nv > 2) w.z = p[2];
+    return w;
+  }
+}
+
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void store16(void* base, int64_t at, int nv, u32x4 w) {
+  if constexpr (BF16) {
+    Raw8<true> r;
+    r.w[0] = w;
+    store_raw8<true, VEC, false>(base, at, nv, r);
+  } else {
+    uint32_t* p = static_cast<uint32_t*>(base) + at;
+    if constexpr (VEC) {
+      *reinterpret_cast<u32x4*>(p) = w;
+    } else if (nv == 4) {
+      *reinterpret_cast<u32x4_a4*>(p) = w;
+    } else {
+      if (nv > 0) p[0] = w.x;
+      if (nv > 1) p[1] = w.y;
+      if (nv > 2) p[2] = w.z;
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack16(u32x4 w, float (&v)[kPer<BF16>]) {
+#pragma unroll
+  for (int j = 0; j < kPer<BF16>; ++j)
+    v[j] = !BF16 ? __uint_as_float(w[j & 3]) : (j & 1) ? bf16_hi(w[(j >> 1) & 3]) : bf16_lo(w[(j >> 1) & 3]);
+}
+
+template <bool BF16>
+__device__ __forceinline__ u32x4 pack16(const float (&v)[kPer<BF16>]) {
+  u32x4 w;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (BF16) w[k] = bf16x2_rne(v[2 * k], v[2 * k + 1]);
+    else w[k] = __float_as_uint(v[k]);
+  }
+  return w;
+}
+
 // One tile after the other (one, but for the longest inputs).  A thread takes chunks kThreads apart: chunk u of
 // head h of token t.  Consecutive lanes hold consecutive chunks, then heads, then tokens.
-template <bool BF16, bool VEC, bool INTERLEAVED>
+template <bool BF16, bool VEC, bool INTERLEAVED, bool STREAM>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, RotaryPlan p) {
+  constexpr int PER = kPer<BF16>;
   extern __shared__ float2 turn[];       // [tokens][pairs]
   const int per_head = p.units, per_token = p.units * p.heads;
   // where a thread's first chunk is, and how far the next one is
   const int u0 = threadIdx.x % per_head, h0 = threadIdx.x / per_head % p.heads, t0 = threadIdx.x / per_token;
   const int du = kThreads % per_head, dh = kThreads / per_head % p.heads, dt = kThreads / per_token;
+  auto load = [&](int64_t at, int nv) { return load16<BF16, VEC, STREAM>(a.x, at, nv); };
   for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
     const int64_t group = tile / p.splits;
     const int head0 = (int)(tile - group * p.splits) * p.heads;
@@ -71,39 +142,42 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, RotaryPl
         const int64_t out = (token0 + t) * a.ldyt + (int64_t)(head0 + h) * a.ldyh;
         const float2* cs = turn + t * a.pairs;
         if constexpr (INTERLEAVED) {
-          const int col = 8 * u, nv = a.D - col < 8 ? a.D - col : 8;
-          const Raw8<BF16> r = load8<BF16, VEC>(a.x, in + col, nv);
-          float v[8];
-          unpack8<BF16, VEC>(r, nv, v);
+          const int col = PER * u, nv = a.D - col < PER ? a.D - col : PER;
+          u32x4 w = load(in + col, nv);
+          if (col < 2 * a.pairs) {
+            float v[PER];
+            unpack16<BF16>(w, v);
 #pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            const int i = 4 * u + j / 2;
-            if (i < a.pairs) {
-              const float2 w = cs[i];
-              const float x = v[j], y = v[j + 1];
-              v[j] = x * w.x - y * w.y;
-              v[j + 1] = y * w.x + x * w.y;
+            for (int j = 0; j < PER; j += 2) {
+              const int i = PER / 2 * u + j / 2;
+              if (i < a.pairs) {
+                const float2 c = cs[i];
+                const float x = v[j], y = v[j + 1];
+                v[j] = x * c.x - y * c.y;
+                v[j + 1] = y * c.x + x * c.y;
+              }
             }
+            w = pack16<BF16>(v);
           }
-          store8<BF16, VEC, false>(a.y, out + col, nv, v);
+          store16<BF16, VEC>(a.y, out + col, nv, w);
         } else if (u < p.turned) {
-          const int col = 8 * u, nv = a.pairs - col < 8 ? a.pairs - col : 8;
-          const Raw8<BF16> ra = load8<BF16, VEC>(a.x, in + col, nv), rb = load8<BF16, VEC>(a.x, in + a.pairs + col, nv);
-          float x[8], y[8];
-          unpack8<BF16, VEC>(ra, nv, x);
-          unpack8<BF16, VEC>(rb, nv, y);
+          const int col = PER * u, nv = a.pairs - col < PER ? a.pairs - col : PER;
+          float x[PER], y[PER];
+          const u32x4 wa = load(in + col, nv), wb = load(in + a.pairs + col, nv);
+          unpack16<BF16>(wa, x);
+          unpack16<BF16>(wb, y);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 w = cs[j < nv ? col + j : 0];
-            const float z = x[j] * w.x - y[j] * w.y;
-            y[j] = y[j] * w.x + x[j] * w.y;
+          for (int j = 0; j < PER; ++j) {
+            const float2 c = cs[j < nv ? col + j : 0];
+            const float z = x[j] * c.x - y[j] * c.y;
+            y[j] = y[j] * c.x + x[j] * c.y;
             x[j] = z;
           }
-          store8<BF16, VEC, false>(a.y, out + col, nv, x);
-          store8<BF16, VEC, false>(a.y, out + a.pairs + col, nv, y);
+          store16<BF16, VEC>(a.y, out + col, nv, pack16<BF16>(x));
+          store16<BF16, VEC>(a.y, out + a.pairs + col, nv, pack16<BF16>(y));
         } else {
-          const int col = 2 * a.pairs + 8 * (u - p.turned), nv = a.D - col < 8 ? a.D - col : 8;
-          store_raw8<BF16, VEC, false>(a.y, out + col, nv, settle8<BF16, VEC>(load8<BF16, VEC>(a.x, in + col, nv), nv));
+          const int col = 2 * a.pairs + PER * (u - p.turned), nv = a.D - col < PER ? a.D - col : PER;
+          store16<BF16, VEC>(a.y, out + col, nv, load(in + col, nv));
         }
       }
       u += du;
@@ -128,17 +202,15 @@ hipError_t launch_rotary(const RotaryArgs& a, hipStream_t st) {
   const int64_t es = a.bf16 ? 2 : 4;
   const bool in_place = a.x == a.y;      // (the strides are then the same: the copied columns are there)
   RotaryPlan p;
-  if (a.interleaved) {
-    p.turned = p.units = (int)(((in_place ? 2 * a.pairs : a.D) + 7) / 8);
-  } else {
-    p.turned = (a.pairs + 7) / 8;
-    p.units = p.turned + (in_place ? 0 : (a.D - 2 * a.pairs + 7) / 8);
-  }
+  const int per = a.bf16 ? 8 : 4;
+  auto chunks = [&](int columns) { return (columns + per - 1) / per; };
+  p.turned = chunks(a.interleaved ? (in_place ? 2 * a.pairs : a.D) : a.pairs);
+  p.units = p.turned + (a.interleaved || in_place ? 0 : chunks(a.D - 2 * a.pairs));
   if (p.units == 0) return hipSuccess;
-  // Tokens whose cosines and sines a workgroup forms together: one a thread, or more where a token has more.
-  p.tokens = std::max(1, std::min(a.pairs ? (kThreads + a.pairs - 1) / a.pairs : 16, 64));
-  // Heads of a tile: about 8 chunks a thread.
-  p.heads = std::max(1, std::min(a.H, 8 * kThreads / (p.tokens * p.units)));
+  // A tile is about kTileChunks chunks: whole tokens, up to those whose cosines and sines are one a thread, or some heads of one.
+  const int64_t token = (int64_t)a.H * p.units;
+  p.tokens = (int)std::max<int64_t>(1, std::min<int64_t>(kTileChunks / token, a.pairs ? (kThreads + a.pairs - 1) / a.pairs : 64));
+  p.heads = (int)std::max<int64_t>(1, std::min<int64_t>(a.H, kTileChunks / ((int64_t)p.tokens * p.units)));
   p.splits = (a.H + p.heads - 1) / p.heads;
   p.heads = (a.H + p.splits - 1) / p.splits;
   p.tiles = (a.T + p.tokens - 1) / p.tokens * p.splits;
@@ -151,14 +223,17 @@ hipError_t launch_rotary(const RotaryArgs& a, hipStream_t st) {
   auto rows = [&](const void* q, int64_t t, int64_t h) {
     return (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && (a.T == 1 || t * es % 16 == 0) && (a.H == 1 || h * es % 16 == 0);
   };
-  const bool vec = a.D % 8 == 0 && (a.interleaved || a.pairs % 8 == 0) &&
+  const bool vec = a.D % per == 0 && (a.interleaved || a.pairs % per == 0) &&
                    rows(a.x, a.ldt, a.ldh) && rows(a.y, a.ldyt, a.ldyh);
-  if (a.bf16) {
-    if (a.interleaved) return vec ? go(rotary_kernel<true, true, true>) : go(rotary_kernel<true, false, true>);
-    return vec ? go(rotary_kernel<true, true, false>) : go(rotary_kernel<true, false, false>);
-  }
-  if (a.interleaved) return vec ? go(rotary_kernel<false, true, true>) : go(rotary_kernel<false, false, true>);
-  return vec ? go(rotary_kernel<false, true, false>) : go(rotary_kernel<false, false, false>);
+  // STREAM: x is read past the caches, where the call moves more than the memory-side cache holds.  32768 x 24 x 128 bf16
+  // 62 us, 76 without; 24576 rows 47.9 and 48.3, 16384 34.1 and 33.6, 8192 18.9 and 16.9.
+  const bool stream = vec && a.T > kMemorySideCache / (2 * es * a.D) / a.H;
+  auto pick = [&](auto bf16, auto interleaved) {
+    constexpr bool B = decltype(bf16)::value, I = decltype(interleaved)::value;
+    return stream ? go(rotary_kernel<B, true, I, true>) : vec ? go(rotary_kernel<B, true, I, false>) : go(rotary_kernel<B, false, I, false>);
+  };
+  if (a.bf16) return a.interleaved ? pick(std::true_type(), std::true_type()) : pick(std::true_type(), std::false_type());
+  return a.interleaved ? pick(std::false_type(), std::true_type()) : pick(std::false_type(), std::false_type());
 }
 
 }  // namespace puro

@@ -36,16 +36,24 @@ typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 typedef u32x2 u32x2_a4 __attribute__((aligned(4)));
 typedef uint32_t u32_a2 __attribute__((aligned(2)));
 
-template <bool BF16, bool VEC>
+// NT: past the caches, for aligned rows of calls that move more than the memory-side cache holds (kMemorySideCache).
+template <bool BF16, bool VEC, bool NT = false>
 __device__ __forceinline__ Raw8<BF16> load8(const void* base, int64_t at, int nv) {
   Raw8<BF16> r;
   r.w[0] = u32x4{0u, 0u, 0u, 0u};
   if constexpr (!BF16) r.w[1] = u32x4{0u, 0u, 0u, 0u};
   if constexpr (VEC) {
+    // (hides that the other side of a branch loads the same: the compiler would make one load of both, and no NT; see apart)
+    if constexpr (NT) asm("" : "+v"(at));
     const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(base) + at * (BF16 ? 2 : 4));
     if (nv > 0) {
-      r.w[0] = p[0];
-      if constexpr (!BF16) r.w[1] = p[1];
+      if constexpr (NT) {
+        r.w[0] = __builtin_nontemporal_load(p);
+        if constexpr (!BF16) r.w[1] = __builtin_nontemporal_load(p + 1);
+      } else {
+        r.w[0] = p[0];
+        if constexpr (!BF16) r.w[1] = p[1];
+      }
     }
   } else if constexpr (BF16) {
     const uint16_t* p = static_cast<const uint16_t*>(base) + at;
@@ -113,6 +121,9 @@ __device__ __forceinline__ void unpack8(const Raw8<BF16>& raw, int nv, float v[8
     }
   }
 }
+
+// At the end of such a branch, for the same reason: the branches' last loads are no common tail.
+__device__ __forceinline__ void apart() { asm volatile(""); }
 
 // The eight values rounded to the row's type.
 template <bool BF16>
@@ -303,6 +314,10 @@ __device__ __forceinline__ void store_codes8(uint8_t* q, float* s, bool ok, bool
     if (first) *s = sc;
   }
 }
+
+// Bytes of the memory-side cache.  A call that moves more finds nothing of what it reads there the next time, and reading past
+// the caches leaves them to what it writes.
+constexpr int64_t kMemorySideCache = 256 << 20;
 
 inline bool vec_row(const void* p, int64_t ld, int64_t es) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * es) % 16 == 0;
