@@ -147,17 +147,17 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, RotaryPl
           if (col < 2 * a.pairs) {
             float v[PER];
             unpack16<BF16>(w, v);
+            const int here = a.pairs - PER / 2 * u;      // pairs of the chunk; columns behind them keep their bits
 #pragma unroll
-            for (int j = 0; j < PER; j += 2) {
-              const int i = PER / 2 * u + j / 2;
-              if (i < a.pairs) {
-                const float2 c = cs[i];
-                const float x = v[j], y = v[j + 1];
-                v[j] = x * c.x - y * c.y;
-                v[j + 1] = y * c.x + x * c.y;
-              }
+            for (int j = 0; j < PER / 2; ++j) {
+              const float2 c = cs[PER / 2 * u + (j < here ? j : 0)];
+              const float x = v[2 * j], y = v[2 * j + 1];
+              v[2 * j] = x * c.x - y * c.y;
+              v[2 * j + 1] = y * c.x + x * c.y;
             }
-            w = pack16<BF16>(v);
+            const u32x4 o = pack16<BF16>(v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = (BF16 ? k : k / 2) < here ? o[k] : w[k];
           }
           store16<BF16, VEC>(a.y, out + col, nv, w);
         } else if (u < p.turned) {
@@ -211,8 +211,8 @@ hipError_t launch_rotary(const RotaryArgs& a, hipStream_t st) {
   const int64_t token = (int64_t)a.H * p.units;
   p.tokens = (int)std::max<int64_t>(1, std::min<int64_t>(kTileChunks / token, a.pairs ? (kThreads + a.pairs - 1) / a.pairs : 64));
   p.heads = (int)std::max<int64_t>(1, std::min<int64_t>(a.H, kTileChunks / ((int64_t)p.tokens * p.units)));
-  p.splits = (a.H + p.heads - 1) / p.heads;
-  p.heads = (a.H + p.splits - 1) / p.splits;
+  p.splits = (int)(((int64_t)a.H + p.heads - 1) / p.heads);
+  p.heads = (int)(((int64_t)a.H + p.splits - 1) / p.splits);
   p.tiles = (a.T + p.tokens - 1) / p.tokens * p.splits;
   const unsigned blocks = (unsigned)std::min<int64_t>(p.tiles, 1 << 22);
   const size_t lds = (size_t)p.tokens * a.pairs * sizeof(float2);

@@ -312,7 +312,9 @@ typedef struct puro_adamw_hyper {
  *   g  = grad * min(1, max_norm / (*norm + 1e-6))
  *   m' = beta1 m + (1 - beta1) g,   v' = beta2 v + (1 - beta2) g g
  *   param' = param (1 - lr weight_decay) - lr / (1 - beta1^step) * m' / (sqrt(v' / (1 - beta2^step)) + eps)
- * in fp32, the hyperparameters' factors rounded once from 64 bits; squares are fp32 (gradients beyond 1.8e19 overflow).
+ * in fp32, the hyperparameters' factors rounded once from 64 bits; squares are fp32 (gradients beyond 1.8e19 overflow).  With
+ * eps = 0 an element whose gradients have all been zero becomes NaN (0 / 0).  A bf16 param without a master loses what
+ * its rounding takes of each step.
  * The step takes m' and v' before they are rounded to 8 bits.  8-bit states are rounded by chance among the two nearest
  * three-bit mantissas, which keeps their expected value, where rounding to the nearest would freeze a state that
  * moves by less than half a code's step; the random bits depend on seed, step, the job's index in the list and the element alone.

@@ -137,6 +137,11 @@ def test_inverse_is_the_gradient(P):
 def test_special_values(P):
     """NaN and infinities stay in their pair; copied columns keep their bits; repeated input (stride 0)."""
     t = torch()
+    for pairs, interleaved, here in itertools.product((1, 2, 5, 13), (False, True), (False, True)):
+        bits = t.randint(-2 ** 15, 2 ** 15, (3, 2, 30), device="cuda").to(t.int16)         # every NaN among them
+        x = bits.view(t.bfloat16).clone()
+        y = P.puro_rotary(x, frequencies(pairs), layout=int(interleaved), y=x if here else None)
+        assert t.equal(y.view(t.int16)[..., 2 * pairs:], bits[..., 2 * pairs:]), (pairs, interleaved, here)
     for dtype, interleaved in itertools.product((t.float32, t.bfloat16), (False, True)):
         x = tensor(6, 2, 29, dtype, 5)
         freqs = frequencies(9)
@@ -210,6 +215,9 @@ def test_past_32_bits(P):
     tail = x[-100:].clone()
     y = P.puro_rotary(x, f, y=x)
     assert t.equal(y[-100:], P.puro_rotary(tail, f, start=T - 100))
+    big = t.randint(-99, 99, (1, (1 << 31) - 1, 1), device="cuda", dtype=t.int8).to(t.bfloat16)     # as many heads as there may be
+    assert t.equal(P.puro_rotary(big, f[:0]), big)
+    del big
     x = t.randn((1 << 25, 1, 2), device="cuda", dtype=t.bfloat16)            # more tiles than workgroups of a launch
     y = P.puro_rotary(x, f[:1])
     assert t.equal(y[-100:], P.puro_rotary(x[-100:], f[:1], start=(1 << 25) - 100))
