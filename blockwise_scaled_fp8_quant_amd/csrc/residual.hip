@@ -28,9 +28,9 @@ namespace {
 // Forward.  Teams, columns and rows as in norm_kernel, and the sums over h' in its order.
 // WHAT: 0 y, 1 codes and scales, 2 h' and the statistics alone (first launch of the dual form).
 // FULL: with a gate or a norm of b (their product with the scale is one vector); else the scale alone.
-// Measured, 16384 x 2048 bf16 RMS: y 46.5 us (5.8 TB/s), h' and statistics 33 (6.1 TB/s) and the codes of both orientations
-// 23 more; one row 3.9 us in a graph: two sums' chains and one trip to memory; 1027 x 1000 fp32 with both norms, layer,
-// 7.4 us: four sums' chains.  4000 x 8192 58.9 us, 2000 x 16384 65.5, both with gate and norm.
+// Measured, bf16 RMS, us: 16384 x 2048 y 44.5 (6.0 TB/s; three sets of inputs and two of outputs in turn), h' and statistics
+// 33 and the codes of both orientations 23 more; one row 4 in a graph: two sums' chains and one trip to memory; 4000 x 8192
+// 59, 2000 x 16384 66 with gate and norm.  1027 x 1000 fp32 with both norms, layer, 7.5: four sums' chains.
 // ---------------------------------------------------------------------------------------------------
 template <bool BF16, bool VEC, int LPR, int ITER, int WHAT, bool FULL>
 __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void residual_kernel(ResidualArgs a) {
@@ -58,6 +58,7 @@ __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void residual_kernel(Residua
   };
   auto fetch = [&](int64_t row) {
     if (VEC && a.stream) {
+      apart();
       load(row, std::integral_constant<bool, VEC>());
       apart();
     } else {
@@ -134,7 +135,13 @@ __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void residual_kernel(Residua
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[j] = __builtin_fmaf(FULL ? f[FULL ? i : 0][j] : a.scale, v[i][j], h[j]);
       const Raw8<BF16> o = pack8<BF16>(h);
-      store_raw8<BF16, VEC, false>(a.h_out, row * n.ldx + col[i], ok ? nv[i] : 0, o);
+      if (VEC && WHAT != 2 && !a.stream) {
+        apart();
+        store_raw8<BF16, VEC, VEC>(a.h_out, row * n.ldx + col[i], ok ? nv[i] : 0, o);
+        apart();
+      } else {
+        store_raw8<BF16, VEC, false>(a.h_out, row * n.ldx + col[i], ok ? nv[i] : 0, o);
+      }
       unpack8<BF16, true>(o, 8, v[i]);
     }
     float mean = 0.f;
@@ -194,12 +201,15 @@ hipError_t launch_fwd(const ResidualArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// Whether a call that moves `passes` times T C elements reads past the caches.  Measured with and without, us, RMS,
-// 2048 columns bf16, inputs in rotation: forward (4 passes) 12288 rows 37.9 and 35.4, 16384 46.5 and 46.7, 32768 84 and
-// 104; backward 12288 rows 37.7 and 38.0 (4 passes), 16384 47.6 and 48.4, with gate and norm (6) 8192 44.0 and 43.2, 12288
-// 58.7 and 60.2, 16384 73.8 and 84.9.
+// Whether a call that moves `passes` times T C elements reads past the caches and leaves them to what it writes; the
+// others write past them, which leaves what they read where it is.  The border, half the memory-side cache, is where the
+// sides meet: us, 2048 columns bf16, three sets of inputs and two of outputs in turn, without - writing past - reading past:
+//   forward (4 passes)       4096 rows 12.6 - 12.5 - 15.5, 8192 26.1 - 22.1 - 24.2, 12288 38.2 - 39.6 - 36.4, 16384 54.3 - 53.7 - 44.5
+//   backward (4)             4096 rows 16.4 - 16.0 - 19.2, 8192 28.3 - 28.4 - 29.9, 12288 41.8 - 40.8 - 40.2, 16384 52.6 - 51.5 - 50.5
+//   with gate and norm (6)   4096 rows 27.1 - 25.7 - 29.5, 8192 47.4 - 45.9 - 44.5, 12288 65.3 - 63.6 - 59.1, 16384 84.6 - 81.1 - 74.5
+// Outputs that alone fill the cache go past it too: 32768 rows with gate and norm 157 - 153 - 151, both 145.
 bool beyond_cache(int64_t T, int64_t C, int64_t es, int passes) {
-  return T > kMemorySideCache / (C * es * passes);
+  return T > kMemorySideCache / 2 / (C * es * passes);
 }
 
 hipError_t launch_residual(ResidualArgs a, hipStream_t st) {

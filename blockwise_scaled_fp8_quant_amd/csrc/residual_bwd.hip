@@ -16,10 +16,10 @@ namespace {
 // thread's columns in registers over the team's rows (in runs of 64, added up in LDS), then over the teams, then written as
 // the workgroup's partial sums and joined in order by a second launch.  FULL: with a gate or a norm of b: one more input and
 // output, a second pair of row sums (b's norm) and the column sum S.
-// Measured, 16384 x 2048 bf16 RMS, inputs in rotation: 44 us (6.1 TB/s) + 4 for the joining; FULL 69 (5.9 TB/s) + 4.6: 565 vector
-// instructions a row and wave keep the vector units 43% busy at two waves per SIMD, whose sums' barriers they meet
-// together.  FULL at 4000 x 8192 83 us, 2000 x 16384 220, of 66 at that rate: there 96 sums and a row's 128 values
-// leave too few of 256 registers, and 384 bytes a lane are spilled.
+// Measured, 16384 x 2048 bf16 RMS, three sets of inputs and two of outputs in turn: 50.7 us with the joining (4 of them; 5.3
+// TB/s), FULL 74.5 (5.4 TB/s): 565 vector instructions a row and wave keep the vector units 43% busy at two waves per SIMD,
+// which meet at the sums' barriers.  FULL at 4000 x 8192 83 us, 2000 x 16384 220, of 74 at that rate: there 96 sums and
+// a row's 128 values leave too few of 256 registers, and 384 bytes a lane are spilled.
 // FULL beyond 4096 columns (a workgroup to a row) keeps the weight and b's factor in LDS, so that nothing spills: a spilled
 // register's reload waits for the row that is loaded ahead.  There is no room for runs then: its launches have a workgroup
 // for every 64 rows.
@@ -131,6 +131,7 @@ __global__ __launch_bounds__(kBwdThreads) void residual_bwd_kernel(ResidualBwdAr
   };
   auto fetch = [&](int64_t r, auto load) {
     if (VEC && a.stream) {
+      apart();
       load(r, std::integral_constant<bool, VEC>());
       apart();
     } else {
@@ -153,6 +154,15 @@ __global__ __launch_bounds__(kBwdThreads) void residual_bwd_kernel(ResidualBwdAr
     const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
     p[0] = add ? p[0] + lo : lo;
     p[1] = add ? p[1] + hi : hi;
+  };
+  auto store = [&](void* base, int64_t at, int n, const float (&v)[8]) {
+    if (VEC && a.past) {
+      apart();
+      store8<BF16, VEC, VEC>(base, at, n, v);
+      apart();
+    } else {
+      store8<BF16, VEC, false>(base, at, n, v);
+    }
   };
   int slot = 0;
   // both sums of a norm's backward pass over the team
@@ -223,7 +233,7 @@ __global__ __launch_bounds__(kBwdThreads) void residual_bwd_kernel(ResidualBwdAr
       unpack8<BF16, VEC>(c2.o[i], nv[i], o);
 #pragma unroll
       for (int j = 0; j < 8; ++j) d[i][j] = __builtin_fmaf(__builtin_fmaf(-xh[i][j], s2, d[i][j]) - s1, c1.rstd, o[j]);
-      store8<BF16, VEC, false>(a.dh, row * a.lddh + col[i], ok ? nv[i] : 0, d[i]);
+      store(a.dh, row * a.lddh + col[i], ok ? nv[i] : 0, d[i]);
       if constexpr (FULL) {
         float w[8];
         vector_of(1, i, w);
@@ -241,7 +251,7 @@ __global__ __launch_bounds__(kBwdThreads) void residual_bwd_kernel(ResidualBwdAr
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = a.scale * d[i][j];
-        store8<BF16, VEC, false>(a.dx, row * a.lddx + col[i], ok ? nv[i] : 0, v);
+        store(a.dx, row * a.lddx + col[i], ok ? nv[i] : 0, v);
       }
     }
     if constexpr (FULL) {
@@ -252,7 +262,7 @@ __global__ __launch_bounds__(kBwdThreads) void residual_bwd_kernel(ResidualBwdAr
 #pragma unroll
           for (int j = 0; j < 8; ++j) d[i][j] = (__builtin_fmaf(-xh[i][j], t2, d[i][j]) - t1) * c2.rstd;
         }
-        store8<BF16, VEC, false>(a.dx, row * a.lddx + col[i], ok ? nv[i] : 0, d[i]);
+        store(a.dx, row * a.lddx + col[i], ok ? nv[i] : 0, d[i]);
       }
     }
     if constexpr (kRuns) {
@@ -398,6 +408,7 @@ hipError_t launch_residual_bwd(ResidualBwdArgs a, hipStream_t st) {
   const int64_t es = a.x_bf16 ? 2 : 4;
   const bool full = a.gate || a.post;
   a.stream = beyond_cache(a.T, a.C, es, full ? 6 : a.dx ? 5 : 4);
+  a.past = !a.stream || a.T >= kMemorySideCache / (a.C * es * (a.dx ? 2 : 1));
   const bool vec = a.C % 8 == 0 && vec_row(a.dy, a.lddy, es) && vec_row(a.h, a.ldh, es) &&
                    (!a.dho || vec_row(a.dho, a.lddho, es)) && (!full || vec_row(a.b, a.ldb, es)) &&
                    vec_row(a.dh, a.lddh, es) && (!a.dx || vec_row(a.dx, a.lddx, es));

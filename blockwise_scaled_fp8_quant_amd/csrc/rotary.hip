@@ -78,11 +78,11 @@ __device__ __forceinline__ void store16(void* base, int64_t at, int nv, u32x4 w)
   if constexpr (BF16) {
     Raw8<true> r;
     r.w[0] = w;
-    store_raw8<true, VEC, false>(base, at, nv, r);
+    store_raw8<true, VEC, VEC>(base, at, nv, r);
   } else {
     uint32_t* p = static_cast<uint32_t*>(base) + at;
     if constexpr (VEC) {
-      *reinterpret_cast<u32x4*>(p) = w;
+      __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p));
     } else if (nv == 4) {
       *reinterpret_cast<u32x4_a4*>(p) = w;
     } else {
@@ -225,8 +225,9 @@ hipError_t launch_rotary(const RotaryArgs& a, hipStream_t st) {
   };
   const bool vec = a.D % per == 0 && (a.interleaved || a.pairs % per == 0) &&
                    rows(a.x, a.ldt, a.ldh) && rows(a.y, a.ldyt, a.ldyh);
-  // STREAM: x is read past the caches, where the call moves more than the memory-side cache holds.  32768 x 24 x 128 bf16
-  // 62 us, 76 without; 24576 rows 47.9 and 48.3, 16384 34.1 and 33.6, 8192 18.9 and 16.9.
+  // y is written past the caches, which leaves x where it is; STREAM: x is read past them too, where the call moves more than
+  // the memory-side cache holds.  us, 24 x 128 bf16, three x and two y in turn, without - writing past - both: 4096 rows 9.6 - 9.7 -
+  // 12.1, 8192 19.5 - 17.1 - 20.9, 16384 40.1 - 34.0 - 38.1, 32768 76.6 - 73.7 - 72.6; fp32 32768 rows 141 - 137 - 127.5.
   const bool stream = vec && a.T > kMemorySideCache / (2 * es * a.D) / a.H;
   auto pick = [&](auto bf16, auto interleaved) {
     constexpr bool B = decltype(bf16)::value, I = decltype(interleaved)::value;

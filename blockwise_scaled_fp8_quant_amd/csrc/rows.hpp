@@ -36,7 +36,7 @@ typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 typedef u32x2 u32x2_a4 __attribute__((aligned(4)));
 typedef uint32_t u32_a2 __attribute__((aligned(2)));
 
-// NT: past the caches, for aligned rows of calls that move more than the memory-side cache holds (kMemorySideCache).
+// NT: past the caches, for aligned rows of large calls (beyond_cache, kMemorySideCache).
 template <bool BF16, bool VEC, bool NT = false>
 __device__ __forceinline__ Raw8<BF16> load8(const void* base, int64_t at, int nv) {
   Raw8<BF16> r;
@@ -122,7 +122,7 @@ __device__ __forceinline__ void unpack8(const Raw8<BF16>& raw, int nv, float v[8
   }
 }
 
-// At the end of such a branch, for the same reason: the branches' last loads are no common tail.
+// At both ends of such a branch, of loads or stores, for the same reason.
 __device__ __forceinline__ void apart() { asm volatile(""); }
 
 // The eight values rounded to the row's type.
@@ -315,8 +315,7 @@ __device__ __forceinline__ void store_codes8(uint8_t* q, float* s, bool ok, bool
   }
 }
 
-// Bytes of the memory-side cache.  A call that moves more finds nothing of what it reads there the next time, and reading past
-// the caches leaves them to what it writes.
+// Bytes of the memory-side cache.
 constexpr int64_t kMemorySideCache = 256 << 20;
 
 inline bool vec_row(const void* p, int64_t ld, int64_t es) {
