@@ -141,6 +141,36 @@ def test_fp8_residual_norm_linear(P):
             assert t.equal(a, b) and t.equal(o, (h + x).view(256, 256)[:T])
 
 
+def test_fp8_residual_norm_linear_of_an_fp32_stream(P):
+    """A residual stream in fp32: the outputs and gradients of the chain of its entry points, bit for bit."""
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.residual import Fp8ResidualNormLinear
+    m = Fp8ResidualNormLinear(256, 384, kind=P.LAYER_NORM, gate=0.5, post_norm=True, scale=0.7, device="cuda")
+    h, x = (t.randn((128, 256), device="cuda", requires_grad=True) for _ in range(2))
+    dy, dho = bf16(128, 384, scale=1e-2), t.randn((128, 256), device="cuda") * 1e-2
+    y, h_out = m(h, x)
+    t.autograd.backward((y, h_out), (dy, dho))
+    n, vec = m.norm, dict(gate=m.norm.gate, post_weight=m.norm.post_weight, scale=0.7)
+    q, s, qT, sT, o, *stats = P.puro_residual_norm_quant_dual(h, x, n.weight, n.bias, **vec)
+    wq, ws, wqT, wsT = P.puro_fp8_quant_w_128x128(m.linear.weight)
+    assert h_out.dtype == t.float32 and t.equal(h_out, o) and t.equal(y, P.puro_fp8_gemm(P.FWD, q, s, wq, ws))
+    gq, gs, gqT, gsT = P.puro_fp8_quant_act_dual(dy)
+    dn = P.puro_fp8_gemm(P.DGRAD, gq, gs, wqT, wsT, out_dtype=P.OUT_FP32)
+    want = P.puro_residual_norm_backward(dn, o, n.weight, *stats[:2], x=x, post_mean=stats[2], post_rstd=stats[3], dh_out=dho, **vec)
+    assert t.equal(h.grad, want[0]) and t.equal(x.grad, want[1])
+    for p, w in zip((n.weight, n.bias, n.gate, n.post_weight), want[2:]):
+        assert t.equal(p.grad, w.bfloat16())
+    assert t.equal(m.linear.weight.grad, P.puro_fp8_gemm(P.WGRAD, gqT, gsT, qT, sT, out_dtype=P.OUT_FP32).bfloat16())
+    # the norm's output alone, the sum alone
+    for outs, grads in (((0,), (dy,)), ((1,), (dho,))):
+        h.grad = x.grad = None
+        both = m(h, x)
+        t.autograd.backward([both[k] for k in outs], grads)
+        want = P.puro_residual_norm_backward(dn if outs == (0,) else t.zeros_like(dn), o, n.weight, *stats[:2], x=x, post_mean=stats[2],
+                                             post_rstd=stats[3], dh_out=dho if outs == (1,) else None, **vec)
+        assert t.equal(h.grad, want[0]) and t.equal(x.grad, want[1])
+
+
 def test_rotary_module(P):
     t = torch()
     from blockwise_scaled_fp8_quant_amd.rotary import Rotary, rotary, rotary_frequencies
@@ -261,6 +291,29 @@ def test_adamw_saves_and_loads(P, bits):
             y, z = other.state[q][name], both[0].state[r][name]
             assert (x == y == z) if name == "step" else x.dtype == y.dtype and t.equal(x, y) and t.equal(x, z)
     assert opt.state[one[0]]["exp_avg"].dtype == (t.uint8 if bits == 8 else t.float32)
+
+
+def test_adamw_with_a_schedule_and_a_rate_on_the_device(P):
+    """A scheduler of torch's sets the rate of both kinds; a capturable optimizer that is loaded goes on with its count."""
+    t = torch()
+    from blockwise_scaled_fp8_quant_amd.adamw import AdamW
+    start = t.randn(333, device="cuda")
+    runs = []
+    for lr, capturable in ((0.5, False), (t.tensor(0.5, device="cuda"), False), (t.tensor(0.5, device="cuda"), True)):
+        p = t.nn.Parameter(start.clone())
+        opt = AdamW([p], lr=lr, state_bits=8, capturable=capturable)
+        schedule = t.optim.lr_scheduler.ExponentialLR(opt, 0.5)
+        for k in range(4):
+            p.grad = bf16(333, seed=k).float()
+            opt.step()
+            schedule.step()
+            if k == 1:
+                other = AdamW([p], lr=lr, state_bits=8, capturable=capturable)
+                other.load_state_dict(opt.state_dict())
+                opt, schedule.optimizer = other, other
+        runs.append((p.detach().clone(), int(opt.state[p]["step"]), float(opt.param_groups[0]["lr"])))
+    for p, step, lr in runs:
+        assert t.equal(p, runs[0][0]) and step == 4 and lr == 0.5 ** 5
 
 
 def test_adamw_refusals(P):
