@@ -120,7 +120,7 @@ __device__ __forceinline__ int find_job(const Table& t, uint32_t chunk) {
 // ---- a thread's elements: PER consecutive ones, nv of them there, behind a uniform base --------------
 // Of element alignment: wide accesses of this target need no more.  (A uniform base and a 32-bit offset are an access
 // without address arithmetic.)  Everything goes past the caches (NT), since no step reads it again soon: 403 M elements with
-// fp32 states 1919 us, without 2064; with 8-bit states 1178 and 1201 (before the last steps).
+// fp32 states 1919 us, without 2064; with 8-bit states 1178 and 1201.
 typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
 
 template <int PER>
@@ -221,7 +221,8 @@ __device__ __forceinline__ void decode8(u32x2 w, float scale, float v[8]) {
 }
 
 // y (at most 448 but for three roundings in magnitude, no NaN) with its mantissa cut to three bits after `chance`, 16
-// bits, is added behind them.  448 and what rounding put above it stay 448: the chance is short of a step by 16 units.
+// bits, is added behind them.  448 and what rounding put above it stay 448: the chance is short of a step by 16 units.  (What
+// rounding put below it stays 448 too, but for a chance of 0, one in 65536.)
 __device__ __forceinline__ float cut(float y, uint32_t chance) {
   return __uint_as_float((__float_as_uint(y) + (chance << 4)) & 0xFFF00000u);
 }

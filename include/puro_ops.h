@@ -301,7 +301,7 @@ typedef struct puro_adamw_hyper {
   double lr, beta1, beta2, eps, weight_decay;   /* finite; 0 <= betas < 1; eps >= 0 (else PURO_ERR_ARG) */
   int64_t step;           /* counted from 1 (else PURO_ERR_ARG) */
   const float* lr_dev;    /* on the device, read by the kernel in place of lr; or NULL */
-  const int64_t* step_dev; /* on the device, read by the kernel in place of step; or NULL */
+  const int64_t* step_dev; /* on the device, read by the kernel in place of step (below 1 its factors are infinite); or NULL */
   const float* norm;      /* on the device: gradients are taken times min(1, max_norm / (*norm + 1e-6)); or NULL */
   float max_norm;         /* >= 0, not NaN (else PURO_ERR_ARG); read with a norm alone */
   uint64_t seed;          /* of the rounding of 8-bit states; the step enters too, so it may stay the same */
