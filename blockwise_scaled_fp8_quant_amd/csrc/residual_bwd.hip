@@ -18,11 +18,14 @@ namespace {
 // output, a second pair of row sums (b's norm) and the column sum S.
 // Measured, 16384 x 2048 bf16 RMS, three sets of inputs and two of outputs in turn: 50.7 us with the joining (4 of them; 5.3
 // TB/s), FULL 74.5 (5.4 TB/s): 565 vector instructions a row and wave keep the vector units 43% busy at two waves per SIMD,
-// which meet at the sums' barriers.  FULL at 4000 x 8192 83 us, 2000 x 16384 220, of 74 at that rate: there 96 sums and
-// a row's 128 values leave too few of 256 registers, and 384 bytes a lane are spilled.
-// FULL beyond 4096 columns (a workgroup to a row) keeps the weight and b's factor in LDS, so that nothing spills: a spilled
-// register's reload waits for the row that is loaded ahead.  There is no room for runs then: its launches have a workgroup
-// for every 64 rows.
+// which meet at the sums' barriers.
+// FULL of 4097 to 8192 columns (a workgroup to a row) keeps the weight and b's factor in LDS, so that nothing spills: a spilled
+// register's reload waits for the row that is loaded ahead.  4000 x 8192: 85 us.
+// Beyond 8192 columns the first and the last column sum stay in LDS and take a row at a time (128 KB at 16384 columns; up to
+// 12288 the weight too), and no row is loaded ahead (loading ahead: 2667 x 12288 bf16 70.5 us, FULL 111.6).  With every sum in
+// registers, which spilled, and without in turn: 2667 x 12288 bf16 91.0 and 70.4 us, FULL 199.2 and 101.5; 2000 x 16384 92.5
+// and 73.2, FULL 186.5 and 154.2 (fp32 294 and 291: FULL at that width still spills 60 to 280 bytes a lane).
+// Both have no room for runs: their launches have a workgroup for every 64 rows.
 // ---------------------------------------------------------------------------------------------------
 constexpr int kBwdThreads = 512;
 constexpr int kRun = 64;               // rows a thread adds in order, and sums of such runs
@@ -47,43 +50,76 @@ __global__ __launch_bounds__(kBwdThreads) void residual_bwd_kernel(ResidualBwdAr
   constexpr int kTeams = kBwdThreads / LPR;
   constexpr int kWidth = 8 * LPR * ITER;
   constexpr int kSums = residual_bwd_sums(FULL);
-  constexpr bool kLds = FULL && LPR == kBwdThreads, kRuns = !kLds;
+  constexpr bool kWide = ITER > 2;                                // sums in LDS
+  constexpr bool kLds = FULL && LPR == kBwdThreads && !kWide;     // vectors in LDS
+  constexpr bool kRuns = !kLds && !kWide;
+  constexpr bool kWeightAgain = FULL && ITER > 3;                 // the weight is read again for each row
+  constexpr bool kWeightLds = kLds || (kWide && ITER < 4);
   __shared__ float red[2][2][kBwdWaves];
   __shared__ __attribute__((aligned(16))) float join[kSums][kRuns ? kTeams * kWidth : 4];
-  __shared__ __attribute__((aligned(16))) float vectors[2][kLds ? kWidth : 4];   // the weight, b's factor
+  __shared__ __attribute__((aligned(16))) float weights[kWeightLds ? kWidth : 4];
+  __shared__ __attribute__((aligned(16))) float factors[kLds ? kWidth : 4];       // of b
+  __shared__ __attribute__((aligned(16))) float held[2][kWide ? kWidth : 4];      // the first sum, the last
   const int team = threadIdx.x / LPR;
   const int tt = threadIdx.x % LPR;
   const int64_t stride = (int64_t)gridDim.x * kTeams;
   const bool post = FULL && a.post != nullptr;
 
   int col[ITER], nv[ITER];
-  float g[kLds ? 1 : ITER][8], f[FULL && !kLds ? ITER : 1][8], sum[kSums][ITER][8];
+  float g[kWeightLds || kWeightAgain ? 1 : ITER][8], f[FULL && !kLds ? ITER : 1][8], sum[kSums][ITER][8];
+  auto in_lds = [](int which) { return kWide && (which == 0 || which == kSums - 1); };
   // eight values at a thread's place in LDS (no other thread touches them)
   auto to_lds = [&](float* base, const float (&v)[8]) {
     reinterpret_cast<f32x4*>(base)[0] = f32x4{v[0], v[1], v[2], v[3]};
     reinterpret_cast<f32x4*>(base)[1] = f32x4{v[4], v[5], v[6], v[7]};
   };
-  auto vector_of = [&](int which, int i, float (&v)[8]) {
-    if constexpr (kLds) {
-      const f32x4* p = reinterpret_cast<const f32x4*>(vectors[which] + col[i]);
-      const f32x4 lo = p[0], hi = p[1];
+  auto from_lds = [&](const float* base, float (&v)[8]) {
+    const f32x4* p = reinterpret_cast<const f32x4*>(base);
+    const f32x4 lo = p[0], hi = p[1];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = lo[j];
-        v[j + 4] = hi[j];
-      }
+    for (int j = 0; j < 4; ++j) {
+      v[j] = lo[j];
+      v[j + 4] = hi[j];
+    }
+  };
+  auto vector_of = [&](int which, int i, float (&v)[8]) {
+    if (which == 0 && kWeightAgain) {
+      int c = col[i];
+      asm volatile("" : "+v"(c));   // or the load moves before the loop, and its registers are spilled
+      load_vec8(a.gamma, a.w_bf16, aligned16(a.gamma), c, nv[i], v);
+    } else if (which == 0 ? kWeightLds : kLds) {
+      from_lds((which == 0 ? weights : factors) + col[i], v);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = which == 0 ? g[i][j] : f[FULL ? i : 0][j];
+      for (int j = 0; j < 8; ++j) v[j] = which == 0 ? g[kWeightLds || kWeightAgain ? 0 : i][j] : f[FULL && !kLds ? i : 0][j];
+    }
+  };
+  // a sum of a thread's eight columns, to be added to and put back
+  auto sum_of = [&](int which, int i, float (&v)[8]) {
+    if (in_lds(which)) {
+      from_lds(held[which != 0] + col[i], v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = sum[which][i][j];
+    }
+  };
+  auto keep_sum = [&](int which, int i, const float (&v)[8]) {
+    if (in_lds(which)) {
+      to_lds(held[which != 0] + col[i], v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[which][i][j] = v[j];
     }
   };
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
     col[i] = 8 * (LPR * i + tt);
     nv[i] = a.C - col[i] < 0 ? 0 : (a.C - col[i] > 8 ? 8 : a.C - col[i]);
-    float (&gi)[8] = g[kLds ? 0 : i];
-    load_vec8(a.gamma, a.w_bf16, aligned16(a.gamma), col[i], nv[i], gi);
-    if constexpr (kLds) to_lds(vectors[0] + col[i], gi);
+    if constexpr (!kWeightAgain) {
+      float (&gi)[8] = g[kWeightLds ? 0 : i];
+      load_vec8(a.gamma, a.w_bf16, aligned16(a.gamma), col[i], nv[i], gi);
+      if constexpr (kWeightLds) to_lds(weights + col[i], gi);
+    }
     if constexpr (FULL) {
       float (&fi)[8] = f[kLds ? 0 : i];
       float w[8];
@@ -94,12 +130,11 @@ __global__ __launch_bounds__(kBwdThreads) void residual_bwd_kernel(ResidualBwdAr
         const float one = j < nv[i] ? 1.f : 0.f;
         fi[j] = a.scale * (a.gate ? fi[j] : one) * (a.post ? w[j] : one);
       }
-      if constexpr (kLds) to_lds(vectors[1] + col[i], fi);
+      if constexpr (kLds) to_lds(factors + col[i], fi);
     }
+    const float none[8] = {};
 #pragma unroll
-    for (int s = 0; s < kSums; ++s)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum[s][i][j] = 0.f;
+    for (int s = 0; s < kSums; ++s) keep_sum(s, i, none);
   }
   const float inv_c = 1.0f / (float)a.C;
   int64_t row = (int64_t)blockIdx.x * kTeams + team;
@@ -188,10 +223,10 @@ __global__ __launch_bounds__(kBwdThreads) void residual_bwd_kernel(ResidualBwdAr
     s2 *= inv_c;
   };
 
-  // The next row is loaded ahead, as far as there are registers: none in the widest class; of four fp32 or unaligned rows the
+  // The next row is loaded ahead, as far as there are registers: none beyond 8192 columns; of four fp32 or unaligned rows the
   // two needed first (8192 x 2047 bf16 56.0 us, 59.9 with all; aligned 16384 x 2048 bf16 77.0 and 73.6 with all), the
   // others while those are worked on.
-  constexpr bool kAhead1 = ITER < 4, kAhead2 = kAhead1 && ((BF16 && VEC) || !FULL);
+  constexpr bool kAhead1 = ITER < 3, kAhead2 = kAhead1 && ((BF16 && VEC) || !FULL);
   if (kAhead1) fetch1(row);
   if (kAhead2) fetch2(row);
   for (int k = 0; k < rows_per_team; ++k, row += stride) {
@@ -208,20 +243,24 @@ __global__ __launch_bounds__(kBwdThreads) void residual_bwd_kernel(ResidualBwdAr
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-      float w[8];
+      float w[8], q0[8], q1[8];
       vector_of(0, i, w);
+      sum_of(0, i, q0);
+      sum_of(1, i, q1);
       unpack8<BF16, VEC>(c1.h[i], nv[i], xh[i]);
       unpack8<BF16, VEC>(c1.y[i], nv[i], d[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // a column that does not exist has dy = 0 and weight 0: it adds nothing to any sum
         xh[i][j] = (xh[i][j] - c1.mean) * c1.rstd;
-        sum[0][i][j] = __builtin_fmaf(d[i][j], xh[i][j], sum[0][i][j]);
-        sum[1][i][j] += d[i][j];
+        q0[j] = __builtin_fmaf(d[i][j], xh[i][j], q0[j]);
+        q1[j] += d[i][j];
         d[i][j] *= w[j];
         s1 += d[i][j];
         s2 = __builtin_fmaf(d[i][j], xh[i][j], s2);
       }
+      keep_sum(0, i, q0);
+      keep_sum(1, i, q1);
     }
     if (!kAhead1) fetch2(row);
     sums_of(s1, s2);
@@ -235,18 +274,20 @@ __global__ __launch_bounds__(kBwdThreads) void residual_bwd_kernel(ResidualBwdAr
       for (int j = 0; j < 8; ++j) d[i][j] = __builtin_fmaf(__builtin_fmaf(-xh[i][j], s2, d[i][j]) - s1, c1.rstd, o[j]);
       store(a.dh, row * a.lddh + col[i], ok ? nv[i] : 0, d[i]);
       if constexpr (FULL) {
-        float w[8];
+        float w[8], q2[8];
         vector_of(1, i, w);
+        sum_of(2, i, q2);
         unpack8<BF16, VEC>(c2.b[i], nv[i], xh[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (post) xh[i][j] = (xh[i][j] - c2.mean) * c2.rstd;
           // (behind the last column D holds -s1 rstd: its place of S is never written, and its factor is 0)
-          sum[2][i][j] = __builtin_fmaf(d[i][j], xh[i][j], sum[2][i][j]);
+          q2[j] = __builtin_fmaf(d[i][j], xh[i][j], q2[j]);
           d[i][j] *= w[j];
           t1 += d[i][j];
           t2 = __builtin_fmaf(d[i][j], xh[i][j], t2);
         }
+        keep_sum(2, i, q2);
       } else if (a.dx) {
         float v[8];
 #pragma unroll
@@ -302,15 +343,18 @@ __global__ __launch_bounds__(kBwdThreads) void residual_bwd_kernel(ResidualBwdAr
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < ITER; ++i)
+      for (int i = 0; i < ITER; ++i) {
+        float v[8];
+        sum_of(which, i, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float s = sum[which][i][j];
+          float s = v[j];
           if constexpr (kRuns) {
             if (runs) s += join[which][col[i] + j];
           }
           if (j < nv[i]) out(which, col[i] + j, s);
         }
+      }
     }
   }
 }
@@ -376,6 +420,7 @@ hipError_t launch_bwd(const ResidualBwdArgs& a, hipStream_t st) {
   else if (a.C <= 2048) e = go(residual_bwd_kernel<BF16, VEC, 128, 2, FULL>);
   else if (a.C <= 4096) e = go(residual_bwd_kernel<BF16, VEC, 256, 2, FULL>);
   else if (a.C <= 8192) e = go(residual_bwd_kernel<BF16, VEC, 512, 2, FULL>);
+  else if (a.C <= 12288) e = go(residual_bwd_kernel<BF16, VEC, 512, 3, FULL>);
   else e = go(residual_bwd_kernel<BF16, VEC, 512, 4, FULL>);
   if (e != hipSuccess || blocks == 1) return e;
   constexpr int kSums = residual_bwd_sums(FULL);
@@ -392,7 +437,7 @@ int residual_bwd_blocks(int64_t T, int64_t C, bool gated) {
   const int64_t teams = kBwdThreads / bwd_lpr(C);
   constexpr int64_t kMost = (int64_t(1) << 32) / kBwdThreads - 1;
   if (T <= 2 * teams) return 1;
-  if (gated && C > 4096 && T > 256 * kRun) return (int)std::min<int64_t>((T + kRun - 1) / kRun, kMost);
+  if (C > (gated ? 4096 : 8192) && T > 256 * kRun) return (int)std::min<int64_t>((T + kRun - 1) / kRun, kMost);
   const int64_t round = (int64_t)kRun * kRun * 256 * teams;
   if (T > round) return (int)(256 * std::min<int64_t>((T + round - 1) / round, kMost / 256));
   return (int)std::min<int64_t>(std::min<int64_t>(256, (T + teams - 1) / teams), std::max<int64_t>(64, (T + 7) / 8));

@@ -133,11 +133,11 @@ def test_residual_backward_refusals():
 
 
 def test_residual_backward_workgroups_grow_with_the_rows():
-    """No team takes more than 64 times 64 rows, and no more than 64 where the kernel adds no runs (a gate or norm of more
-    than 4096 columns); a launch has fewer than 2^32 threads."""
+    """No team takes more than 64 times 64 rows, and no more than 64 where the kernel adds no runs (more than 8192
+    columns, with a gate or norm more than 4096); a launch has fewer than 2^32 threads."""
     for C, lanes in ((8, 16), (128, 16), (200, 32), (1000, 64), (2000, 128), (4096, 256), (4104, 512), (8200, 512), (16384, 512)):
         for gated in (False, True):
-            most = 64 if gated and C > 4096 else 4096
+            most = 64 if C > (4096 if gated else 8192) else 4096
             for T in (1000, 16384, 262145, 1 << 20, (1 << 20) + 1, 10 ** 7):
                 blocks = max(P.puro_residual_norm_backward_workspace_size(T, C, gated) // (4 * (3 if gated else 2) * C), 1)
                 assert blocks * (512 // lanes) * most >= T and blocks * 512 < 1 << 32

@@ -157,7 +157,7 @@ def backward_reference(dy, dho, h_out, x, vec, stats, scale, kind):
 @pytest.mark.parametrize("gate,post,scale", FORMS)
 @pytest.mark.parametrize("T,C", [(1, 1), (1, 8), (2, 7), (17, 100), (90, 128), (200, 200), (65, 512), (300, 1000), (40, 2048), (513, 2048),
                                  (33, 4100), (9, 8192), (1, 16384), (19, 16376), (4500, 256), (6001, 2048), (1300, 8192),
-                                 (40000, 120), (20000, 8200)])
+                                 (40000, 120), (20000, 8200), (3, 12288), (600, 12280), (70, 12281), (2, 12289), (300, 14000)])
 def test_backward(P, T, C, gate, post, scale):
     t = torch()
     types = ((t.bfloat16, t.bfloat16), (t.float32, t.float32), (t.bfloat16, t.float32))
