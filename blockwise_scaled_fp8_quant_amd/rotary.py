@@ -95,12 +95,25 @@ class Rotary(torch.nn.Module):
         super().__init__()
         self.columns, self.base, self.layout, self.scaling = columns, base, layout, scaling
         # no buffer: a module's cast to another type would round the frequencies
-        self._freqs, self.scale = rotary_frequencies(columns, base, scaling, **how)
+        with torch.inference_mode(False):
+            self._freqs, self.scale = rotary_frequencies(columns, base, scaling, **how)
+        self._copies = {self._freqs.device: self._freqs}
+
+    def frequencies(self, device):
+        """The frequencies on a device, copied there once.  The copy serves every later call, those with gradients too, whatever
+        mode the first one is made in."""
+        found = self._copies.get(device)
+        if found is None:
+            if device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("a step is being captured before the frequencies are on its GPU: make the module there "
+                                   "(device=), or one eager call first")
+            with torch.inference_mode(False):
+                # (from host memory, which the copy waits for: any stream may read it then)
+                found = self._copies.setdefault(device, self._freqs.cpu().to(device))
+        return found
 
     def forward(self, x, positions=None, start: int = 0):
-        if self._freqs.device != x.device:
-            self._freqs = self._freqs.to(x.device)
-        return rotary(x, self._freqs, positions, start, self.layout, self.scale)
+        return rotary(x, self.frequencies(x.device), positions, start, self.layout, self.scale)
 
     def extra_repr(self) -> str:
         return f"{self.columns}, base={self.base}, scaling={self.scaling}"
