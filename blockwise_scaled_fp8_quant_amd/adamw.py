@@ -86,10 +86,15 @@ class AdamW(torch.optim.Optimizer):
                     return [s.get(name) for s in states] if any(name in s for s in states) else None
                 if group["capturable"]:
                     step.add_(1)
-                puro_adamw(params, grads, column("exp_avg"), column("exp_avg_sq"), step, group["lr"], *group["betas"],
-                           group["eps"], group["weight_decay"], masters=column("master"), avg_scales=column("avg_scale"),
-                           sq_scales=column("sq_scale"), norm=norm, max_norm=1.0 if norm is None else max_norm,
-                           seed=(group["seed"] + k * 0x9E3779B97F4A7C15) % 2 ** 64)
+                try:
+                    puro_adamw(params, grads, column("exp_avg"), column("exp_avg_sq"), step, group["lr"], *group["betas"],
+                               group["eps"], group["weight_decay"], masters=column("master"), avg_scales=column("avg_scale"),
+                               sq_scales=column("sq_scale"), norm=norm, max_norm=1.0 if norm is None else max_norm,
+                               seed=(group["seed"] + k * 0x9E3779B97F4A7C15) % 2 ** 64)
+                except Exception:
+                    if group["capturable"]:
+                        step.sub_(1)                  # a refused step is none
+                    raise
                 if not group["capturable"]:
                     for s in states:
                         s["step"] = step
