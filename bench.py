@@ -60,8 +60,8 @@ COPY_BYTES = 256 << 20          # calibration copy: 256 MiB read + 256 MiB writt
 
 
 # operators that no step here launches (norm, residual sum, rotary positions, clipping, AdamW, few-row product)
-OTHER_SOURCES = ("adamw.hip", "clip.hip", "gemm_rows.hip", "norm.hip", "ops_internal.hpp", "residual.hip",
-                 "residual_bwd.hip", "rotary.hip", "rows.hpp")
+OTHER_SOURCES = ("adamw.hip", "clip.hip", "gemm_rows.hip", "norm.hip", "ops_internal.hpp", "overlap.hpp",
+                 "residual.hip", "residual_bwd.hip", "rotary.hip", "rows.hpp")
 
 
 def kernel_source_hash() -> str:

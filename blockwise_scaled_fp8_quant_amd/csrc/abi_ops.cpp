@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "ops_internal.hpp"
+#include "overlap.hpp"
 
 namespace {
 
@@ -160,6 +161,19 @@ int check_residual(const puro_residual* r, int64_t align, puro::ResidualArgs& a)
   a.gate = r->gate; a.post = r->post_weight; a.scale = r->scale;
   a.post_mean = r->post_mean; a.post_rstd = r->post_rstd;
   return PURO_OK;
+}
+
+// What the forward forms read and write but for the norm: h_out may be h or x, and so may another matrix that replaces.
+puro::Tensors residual_tensors(const puro_residual& r) {
+  using namespace puro;
+  const int64_t es = size_of(r.x_dtype), vec = r.C * size_of(r.w_dtype), stat = r.T * 4;
+  Tensors t;
+  t.reads(r.h, replacing(matrix(r.h, r.T, r.ldh, r.C, es)));
+  t.reads(r.x, replacing(matrix(r.x, r.T, r.ldx, r.C, es)));
+  for (const void* p : {r.weight, r.bias, r.gate, r.post_weight}) t.reads(p, vector(p, vec));
+  t.writes(r.h_out, replacing(matrix(r.h_out, r.T, r.ldh_out, r.C, es)));
+  for (const void* p : {r.mean, r.rstd, r.post_mean, r.post_rstd}) t.writes(p, vector(p, stat));
+  return t;
 }
 
 // Whether the D-wide heads of [T, H, D] with these strides lie apart from each other.
@@ -395,7 +409,9 @@ int puro_residual_norm(const puro_residual* r, void* y, int64_t ldy, hipStream_t
   if (!y) return PURO_ERR_NULLPTR;
   if (!aligned(y, size_of(r->x_dtype))) return PURO_ERR_ALIGN;
   if (ldy < r->C) return PURO_ERR_LD;
-  if (y == r->h_out) return PURO_ERR_ARG;
+  puro::Tensors t = residual_tensors(*r);
+  t.writes(y, puro::replacing(puro::matrix(y, r->T, ldy, r->C, size_of(r->x_dtype))));
+  if (t.clash()) return PURO_ERR_ARG;
   a.n.y = y; a.n.ldy = ldy;
   return from_hip(puro::launch_residual(a, st));
 }
@@ -408,6 +424,10 @@ int puro_residual_norm_quant(const puro_residual* r, uint8_t* q, int64_t ldq, fl
   if (!q || !s) return PURO_ERR_NULLPTR;
   if (!aligned(q, 16) || !aligned(s, 16)) return PURO_ERR_ALIGN;
   if (ldq < r->C || ldq % 16) return PURO_ERR_LD;
+  puro::Tensors t = residual_tensors(*r);
+  t.writes(q, puro::matrix(q, r->T, ldq, r->C, 1));
+  t.writes(s, puro::vector(s, r->C / kGroup * r->T * 4));
+  if (t.clash()) return PURO_ERR_ARG;
   a.n.q = q; a.n.ldq = ldq; a.n.s = s;
   return from_hip(puro::launch_residual_quant(a, st));
 }
@@ -422,6 +442,12 @@ int puro_residual_norm_quant_dual(const puro_residual* r, uint8_t* q, int64_t ld
   if (!aligned(q, 16) || !aligned(s, 16) || !aligned(qT, 16) || !aligned(sT, 16)) return PURO_ERR_ALIGN;
   if (ldq < r->C || ldq % 16 || ldqT < r->T || ldqT % 16) return PURO_ERR_LD;
   if (too_many_blocks(r->T / kGroup, r->C / kGroup)) return PURO_ERR_UNSUPPORTED;
+  puro::Tensors t = residual_tensors(*r);
+  t.writes(q, puro::matrix(q, r->T, ldq, r->C, 1));
+  t.writes(s, puro::vector(s, r->C / kGroup * r->T * 4));
+  t.writes(qT, puro::matrix(qT, r->C, ldqT, r->T, 1));
+  t.writes(sT, puro::vector(sT, r->T / kGroup * r->C * 4));
+  if (t.clash()) return PURO_ERR_ARG;
   a.n.q = q; a.n.ldq = ldq; a.n.s = s;
   a.n.qT = qT; a.n.ldqT = ldqT; a.n.sT = sT;
   return from_hip(puro::launch_residual_quant_dual(a, st));
@@ -462,10 +488,22 @@ int puro_residual_norm_backward(const puro_residual_grad* r, void* workspace, si
     if (r->lddy < r->C || r->ldh_out < r->C || r->lddh < r->C || (r->dh_out && r->lddh_out < r->C) ||
         (gated && r->ldx < r->C) || (r->dx && r->lddx < r->C))
       return PURO_ERR_LD;
-    if (r->dx == r->dh) return PURO_ERR_ARG;
     const size_t need = puro_residual_norm_backward_workspace_size(r->T, r->C, gated);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return PURO_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 16)) return PURO_ERR_ALIGN;
+    using namespace puro;
+    Tensors t;
+    t.reads(r->dy, replacing(matrix(r->dy, r->T, r->lddy, r->C, es)));
+    t.reads(r->h_out, replacing(matrix(r->h_out, r->T, r->ldh_out, r->C, es)));
+    t.reads(r->dh_out, replacing(matrix(r->dh_out, r->T, r->lddh_out, r->C, es)));
+    if (gated) t.reads(r->x, replacing(matrix(r->x, r->T, r->ldx, r->C, es)));
+    for (const void* p : {r->weight, r->gate, r->post_weight}) t.reads(p, vector(p, r->C * ws));
+    for (const void* p : {r->mean, r->rstd, r->post_mean, r->post_rstd}) t.reads(p, vector(p, r->T * 4));
+    t.writes(r->dh, replacing(matrix(r->dh, r->T, r->lddh, r->C, es)));
+    t.writes(r->dx, replacing(matrix(r->dx, r->T, r->lddx, r->C, es)));
+    for (const void* p : {r->dweight, r->dbias, r->dgate, r->dpost_weight}) t.writes(p, vector(p, r->C * 4));
+    if (need > 0) t.writes(workspace, vector(workspace, need));
+    if (t.clash()) return PURO_ERR_ARG;
   }
   puro::ResidualBwdArgs a = {};
   a.dy = r->dy; a.lddy = r->lddy; a.h = r->h_out; a.ldh = r->ldh_out; a.dho = r->dh_out; a.lddho = r->lddh_out;

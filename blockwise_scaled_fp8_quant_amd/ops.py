@@ -235,7 +235,8 @@ def puro_residual_norm(h, x, weight, bias=None, eps: float = 1e-5, kind: int = L
     """(y, h_out, mean, rstd, post_mean, post_rstd) of the residual stream h and a block's output x, both [T, C] bf16 or
     fp32: h_out = h + scale * gate * p, with p = x or, with post_weight, norm(x) * post_weight, and y the layer or RMS
     norm of h_out with weight and bias.  gate and post_weight [C], of weight's type.  The statistics are those the backward pass
-    takes (None where there are none; with stats=False only those given are written).  Each of h_out and y may be h or x."""
+    takes (None where there are none; with stats=False only those given are written).  Each of h_out and y may be h or x; outputs that
+    share memory with another tensor of the call otherwise are refused, here and in the forms below."""
     return _on(stream, _marshal.residual_norm)(h, x, weight, bias, eps, kind, gate, post_weight, scale, h_out, mean, rstd,
                                                post_mean, post_rstd, y, stats)
 
@@ -269,7 +270,7 @@ def puro_residual_norm_backward(dy, h_out, weight, mean, rstd, x=None, gate=None
     """(dh, dx, dweight, dbias, dgate, dpost_weight): the backward pass of puro_residual_norm from the gradients of y (dy) and
     of h_out (dh_out, None for zero) and what the forward pass left.  x is needed with a gate or a post_weight.  dh and
     dx [T, C] of x's type (without gate, post_weight, scale and a dx given, dx is dh itself); the others fp32 [C], None where
-    there is no such vector.  accumulate adds to those given.  dh may be dy or dh_out; dx may be x."""
+    there is no such vector.  accumulate adds to those given.  dh and dx may each be one of dy, h_out, dh_out and x."""
     return _on(stream, _marshal.residual_norm_backward)(dy, h_out, weight, mean, rstd, x, gate, post_weight, post_mean, post_rstd,
                                                         dh_out, scale, kind, dh, dx, dweight, dbias, dgate, dpost_weight,
                                                         with_bias, accumulate, workspace)

@@ -167,6 +167,8 @@ size_t puro_gemm_rows_workspace_size(int64_t M, int64_t N, int64_t K);
  *   y     = norm(h_out) * weight + bias
  * The norm is that of h_out as it is written: y, mean and rstd (or the codes and scales) are those that puro_layer_norm
  * (puro_layer_norm_quant, ..._dual) gives for it, bit for bit.
+ * h_out may be h or x (same pointer and stride).  Other than that nothing that is written may share memory with anything else
+ * that the call reads or writes (PURO_ERR_ARG); rows of one buffer whose columns lie side by side share none.
  */
 typedef struct puro_residual {
   int kind;               /* PURO_NORM_LAYER, PURO_NORM_RMS: of both norms */
@@ -192,8 +194,7 @@ typedef struct puro_residual {
 } puro_residual;
 
 /*
- * The norm as a tensor: y [T, C] of x_dtype, row stride ldy.  Each of h_out and y may be h or x (same pointer and stride), but
- * not both the same tensor (PURO_ERR_ARG).  Rows need element alignment, as in puro_layer_norm.
+ * The norm as a tensor: y [T, C] of x_dtype, row stride ldy.  As h_out, y may be h or x, but not both the same tensor.  Rows need element alignment, as in puro_layer_norm.
  * The struct is read before the call returns.
  */
 int puro_residual_norm(const puro_residual* r, void* y, int64_t ldy, hipStream_t st);
@@ -239,10 +240,10 @@ typedef struct puro_residual_grad {
   const float* rstd;
   const float* post_mean; /* with post_weight alone (else NULL, or PURO_ERR_ARG) */
   const float* post_rstd;
-  void* dh;               /* [T, C] of x_dtype; may be dy or dh_out (same pointer and stride) */
+  void* dh;               /* [T, C] of x_dtype */
   int64_t lddh;
-  void* dx;               /* [T, C] of x_dtype; may be x, or dy or dh_out where dh is not; never dh (PURO_ERR_ARG).  NULL without */
-  int64_t lddx;           /* gate and post_weight: not written (with scale 1 it equals dh) */
+  void* dx;               /* [T, C] of x_dtype.  NULL without gate and post_weight: not written (with scale 1 it equals dh) */
+  int64_t lddx;
   float* dweight;         /* fp32 [C] */
   float* dbias;           /* fp32 [C] or NULL */
   float* dgate;           /* fp32 [C] or NULL; without a gate NULL (else PURO_ERR_ARG) */
@@ -253,6 +254,8 @@ typedef struct puro_residual_grad {
 /*
  * workspace: puro_residual_norm_backward_workspace_size(T, C, gated) bytes, gated = 1 with a gate or a post_weight; 16-byte
  * aligned (NULL when 0).  T == 0 (or C == 0) writes no dh and dx; with accumulate = 0 it still sets the sums to zero.
+ * dh and dx may each be one of dy, h_out, dh_out and x (same pointer and stride), not both the same.  Other than that nothing that
+ * is written, the used part of the workspace included, may share memory with anything else of the call (PURO_ERR_ARG).
  */
 int puro_residual_norm_backward(const puro_residual_grad* r, void* workspace, size_t workspace_bytes, hipStream_t st);
 size_t puro_residual_norm_backward_workspace_size(int64_t T, int64_t C, int gated);

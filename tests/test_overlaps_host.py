@@ -1,0 +1,93 @@
+"""Calls whose outputs share memory with what they read or write elsewhere are refused on the host (no GPU, no kernel launched:
+every call below is refused).  Rows are laid out by brute force, cell by cell, beside the library's arithmetic."""
+import random
+
+from test_block_ops_host import A, ARG, BF16, FP32, GRAD, RES, back, dual, quant, residual
+
+ES = {BF16: 2, FP32: 4}
+
+
+def rows_of(p, n, ld, columns, es):
+    return {(p // es + i * ld) * es + b for i in range(n) for c in range(columns) for b in range(c * es, c * es + es)}
+
+
+# bytes of each operand of a call on RES / GRAD's shapes
+def sizes(base, **more):
+    T, C = base["T"], base["C"]
+    matrix, vector, stat = 2 * T * C, 2 * C, 4 * T
+    return {**{k: matrix for k in ("h", "x", "h_out", "y", "dy", "dh_out", "dh", "dx")}, **{k: vector for k in ("weight", "bias", "gate", "post_weight")},
+            **{k: stat for k in ("mean", "rstd", "post_mean", "post_rstd")}, **{k: 4 * C for k in ("dweight", "dbias", "dgate", "dpost_weight")}, **more}
+
+
+def ends(base, size, align):
+    """Places at which `size` bytes overlap those of `base` = (address, bytes): their ends by one unit, and the middle."""
+    at, n = base
+    up = lambda v: -(-v // align) * align
+    return {up(at - size + align) if size > align else at, at, at + up(n) - align if up(n) > align else at}
+
+
+def clashes(call, place, size, read, written, align, free):
+    """Every written operand over every other one (free: pairs that may be the same tensor, at the same place)."""
+    for out in written:
+        for other in (*read, *written):
+            if other == out:
+                continue
+            for at in ends((place[other], size[other]), size[out], align):
+                if at == place[other] and (out, other) in free:
+                    continue
+                assert call(**{out: at}) == ARG, (out, other, at - place[other])
+
+
+IN, STATS = ("h", "x", "weight", "bias", "gate", "post_weight"), ("mean", "rstd", "post_mean", "post_rstd")
+REPLACED = {(o, i) for o in ("h_out", "y") for i in ("h", "x")}
+
+
+def test_residual():
+    clashes(residual, {**RES, "y": A[11]}, sizes(RES), IN, ("h_out", "y", *STATS), 4, REPLACED)
+    for T in (2, 4):                                                 # in place, but with another stride
+        for out, given in REPLACED:
+            ld = {"y": "ldy", "h_out": "ldh_out"}[out]
+            assert residual(**{"T": T, out: RES[given], ld: 264}) == ARG
+    assert residual(h_out=RES["h"], y=RES["h"]) == ARG and residual(h_out=RES["x"], y=RES["x"]) == ARG
+
+
+def test_residual_codes():
+    size = sizes(RES, q=4 * 256, s=4 * 2 * 4)
+    clashes(quant, {**RES, "q": A[11], "s": A[12]}, size, IN, ("h_out", "q", "s"), 16, REPLACED)
+    size = sizes({**RES, "T": 256}, q=256 * 256, s=4 * 2 * 256, qT=256 * 256, sT=4 * 2 * 256)
+    clashes(dual, {**RES, "q": A[11], "s": A[12], "qT": A[13], "sT": A[14]}, size, IN,
+            ("h_out", "q", "s", "qT", "sT", "mean", "rstd"), 16, REPLACED)
+
+
+def test_residual_backward():
+    place = {**GRAD, "dbias": A[13] + 8192, "ws": 1 << 36}
+    read = ("dy", "h_out", "dh_out", "x", "weight", "gate", "post_weight", *STATS)
+    written = ("dh", "dx", "dweight", "dbias", "dgate", "dpost_weight")
+    free = {(o, i) for o in ("dh", "dx") for i in ("dy", "h_out", "dh_out", "x")}
+    call = lambda **k: back(**{"dbias": place["dbias"], "ws": place["ws"], **k})
+    clashes(call, place, sizes(GRAD), read, written, 4, free)
+    from blockwise_scaled_fp8_quant_amd import puro_residual_norm_backward_workspace_size as need
+    assert need(64, 256, True) > 0
+    for other in (*read, *written):                                  # the workspace over anything
+        assert call(ws=place[other] // 16 * 16) == ARG and call(ws=place[other] - need(64, 256, True) + 16) == ARG, other
+    for out, ld in (("dh", "lddh"), ("dx", "lddx")):
+        for given in ("dy", "h_out", "dh_out", "x"):
+            assert call(**{out: place[given], ld: 264}) == ARG, (out, given)
+    assert call(dh=place["dy"], dx=place["dy"]) == ARG
+
+
+def test_rows_that_interleave():
+    """h_out laid over h in one buffer with strides of its own: refused where a cell is in both."""
+    rng = random.Random(3)
+    base, seen = 1 << 33, 0
+    for _ in range(4000):
+        T, C = rng.randint(1, 6), rng.randint(1, 8)
+        ld = C + rng.randint(0, 12)
+        other = ld if rng.random() < 0.5 else C + rng.randint(0, 20)
+        at = base + 4 * rng.randint(0, 80)
+        if at == base and (T == 1 or ld == other):
+            continue
+        if rows_of(at, T, other, C, 4) & rows_of(base, T, ld, C, 4):
+            seen += 1
+            assert residual(x_dtype=FP32, T=T, C=C, h=base, ldh=ld, ldx=C, h_out=at, ldh_out=other, ldy=C) == ARG, (T, C, ld, other, at - base)
+    assert seen > 1000
