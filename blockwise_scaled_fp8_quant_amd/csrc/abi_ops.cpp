@@ -531,8 +531,20 @@ int puro_rotary(int x_dtype, int layout, int inverse, const void* x, int64_t ld_
   const int64_t es = size_of(x_dtype);
   if (!aligned(x, es) || !aligned(y, es) || !aligned(freqs, 8) || !aligned(positions, 8)) return PURO_ERR_ALIGN;
   if (ld_t < 0 || ld_h < 0 || !heads_apart(T, H, D, ldy_t, ldy_h)) return PURO_ERR_LD;
-  if (x == y && ((T > 1 && ld_t != ldy_t) || (H > 1 && ld_h != ldy_h))) return PURO_ERR_ARG;
   if (T > kIntMax || H > kIntMax || D > (int64_t(1) << 30) || pairs > puro::kRotaryMaxPairs) return PURO_ERR_UNSUPPORTED;
+  puro::Tensors t;
+  const bool tokens_first = H <= 1 || T <= 1 || ldy_t >= ldy_h;      // (heads_apart: the longer stride is the outer one)
+  auto heads = [&](const void* p, int64_t ldt, int64_t ldh) {
+    puro::Rows r = puro::matrix(p, tokens_first ? T : H, tokens_first ? ldt : ldh, D, es);
+    r.rows = tokens_first ? H : T;
+    r.ld_row = (puro::Rows::wide)(tokens_first ? ldh : ldt) * es;
+    return puro::replacing(r);
+  };
+  t.reads(x, heads(x, ld_t, ld_h));
+  t.reads(positions, puro::vector(positions, T * 8));
+  t.reads(freqs, puro::vector(freqs, pairs * 8));
+  t.writes(y, heads(y, ldy_t, ldy_h));
+  if (t.clash()) return PURO_ERR_ARG;
   puro::RotaryArgs a = {};
   a.x = x; a.ldt = ld_t; a.ldh = ld_h;
   a.y = y; a.ldyt = ldy_t; a.ldyh = ldy_h;

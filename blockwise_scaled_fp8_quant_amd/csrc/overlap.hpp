@@ -103,10 +103,10 @@ inline bool share_memory(Rows a, const Rows& b) {
 class Tensors {
  public:
   void reads(const void* p, const Rows& r) {
-    if (p) in_[n_in_++] = r;
+    if (p && r.width > 0) in_[n_in_++] = r;
   }
   void writes(const void* p, const Rows& r) {
-    if (p) out_[n_out_++] = r;
+    if (p && r.width > 0) out_[n_out_++] = r;
   }
   // Whether one that is written shares memory with another that it does not replace.
   bool clash() const {

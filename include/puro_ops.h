@@ -194,7 +194,8 @@ typedef struct puro_residual {
 } puro_residual;
 
 /*
- * The norm as a tensor: y [T, C] of x_dtype, row stride ldy.  As h_out, y may be h or x, but not both the same tensor.  Rows need element alignment, as in puro_layer_norm.
+ * The norm as a tensor: y [T, C] of x_dtype, row stride ldy.  As h_out, y may be h or x, but not both the same tensor.  Rows
+ * need element alignment, as in puro_layer_norm.
  * The struct is read before the call returns.
  */
 int puro_residual_norm(const puro_residual* r, void* y, int64_t ldy, hipStream_t st);
@@ -272,8 +273,8 @@ enum { PURO_ROTARY_HALF = 0, PURO_ROTARY_INTERLEAVED = 1 };
  *   positions : int64 [T] on the device, or NULL: token t is at start + t.
  *   freqs : fp64 [pairs] on the device, radians a position; 2 * pairs <= D, pairs <= 2048.
  *   scale : finite (else PURO_ERR_ARG); of the turned columns alone, where a long-context scaling has one.
- *   y : [T, H, D] of x_dtype with its own strides; y may be x, with the same strides (else PURO_ERR_ARG); other than that
- *       they do not overlap.
+ *   y : [T, H, D] of x_dtype with its own strides; y may be x, with the same strides; other than that it may not share memory
+ *       with x, positions or freqs (PURO_ERR_ARG; heads of one buffer beside each other share none).
  * Angles are formed and reduced in 64 bits: position * freq is off by 2^-53 of itself.  Positions beyond 2^53 are rounded.
  * Strides of y that put two heads over each other are refused (PURO_ERR_LD): tokens lie apart from each other with all their
  * heads, or heads with all their tokens.  x may repeat (stride 0).  T, H < 2^31, D <= 2^30.

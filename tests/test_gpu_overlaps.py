@@ -120,3 +120,50 @@ def test_refusals_write_nothing(P):
             call()
             raise AssertionError(f"call {k} was not refused")
     assert all(t.equal(a, b) for a, b in zip((h, x, w), kept)) and not two.any()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_heads_of_one_buffer(P, dtype):
+    """A turned half of the heads beside the given one, tokens or heads outermost, or a part of every head beside the rest."""
+    t = torch()
+    dt = getattr(t, dtype)
+    freqs = t.logspace(0, -3, 8, dtype=t.float64, device="cuda")
+    for shape, cut in (((50, 8, 32), lambda b, k: b[:, 4 * k: 4 * k + 4]), ((50, 8, 32), lambda b, k: b[:, k::2]),
+                       ((8, 50, 32), lambda b, k: b.transpose(0, 1)[:, 4 * k: 4 * k + 4]), ((50, 4, 64), lambda b, k: b[..., 32 * k: 32 * k + 32]),
+                       ((1, 8, 32), lambda b, k: b[:, 4 * k: 4 * k + 4]), ((50, 1, 64), lambda b, k: b[..., 32 * k: 32 * k + 32])):
+        say(f"[overlaps] heads {shape} {dtype}")
+        b = t.randn(shape, device="cuda").to(dt)
+        x = cut(b, 0).clone()
+        for layout in (0, 1):
+            want = P.puro_rotary(x, freqs, layout=layout)
+            assert t.equal(P.puro_rotary(cut(b, 0), freqs, layout=layout, y=cut(b, 1)), want) and t.equal(cut(b, 0), x)
+
+
+def test_heads_that_interleave(P):
+    """x and y laid over each other at random: refused with nothing written where a cell is in both, else the result."""
+    t = torch()
+    rng = random.Random(6)
+    freqs = t.ones(1, dtype=t.float64, device="cuda")
+    clear = clash = 0
+    for _ in range(400):
+        T, H, D = rng.randint(1, 4), rng.randint(1, 4), rng.randint(2, 6)
+        inner = D + rng.randint(0, 8)
+        outer = (max(T, H) - 1) * inner + D + rng.randint(0, 20)
+        ldy = (outer, inner) if rng.random() < 0.5 else (inner, outer)
+        ldx = ldy if rng.random() < 0.6 else (rng.randint(0, 30), rng.randint(0, 30))
+        a, b = rng.randint(0, 120), rng.randint(0, 120)
+        buffer = t.randn(600, device="cuda")
+        before = buffer.clone()
+        x, y = buffer.as_strided((T, H, D), (*ldx, 1), a), buffer.as_strided((T, H, D), (*ldy, 1), b)
+        cells = lambda at, ld: {at + i * ld[0] + k * ld[1] + d for i in range(T) for k in range(H) for d in range(D)}
+        inside = a == b and (T == 1 or ldx[0] == ldy[0]) and (H == 1 or ldx[1] == ldy[1])
+        if cells(a, ldx) & cells(b, ldy) and not inside:
+            clash += 1
+            with pytest.raises(P.PuroError):
+                P.puro_rotary(x, freqs, y=y)
+            assert t.equal(buffer, before)
+        else:
+            clear += 1
+            want = P.puro_rotary(x.clone(), freqs)
+            assert t.equal(P.puro_rotary(x, freqs, y=y), want)
+    assert clear > 50 and clash > 50

@@ -2,7 +2,7 @@
 every call below is refused).  Rows are laid out by brute force, cell by cell, beside the library's arithmetic."""
 import random
 
-from test_block_ops_host import A, ARG, BF16, FP32, GRAD, RES, back, dual, quant, residual
+from test_block_ops_host import A, ARG, BF16, FP32, GRAD, RES, back, dual, quant, residual, rotary
 
 ES = {BF16: 2, FP32: 4}
 
@@ -91,3 +91,46 @@ def test_rows_that_interleave():
             seen += 1
             assert residual(x_dtype=FP32, T=T, C=C, h=base, ldh=ld, ldx=C, h_out=at, ldh_out=other, ldy=C) == ARG, (T, C, ld, other, at - base)
     assert seen > 1000
+
+
+def heads_of(p, T, H, D, ld_t, ld_h):
+    return {p + i * ld_t + k * ld_h + d for i in range(T) for k in range(H) for d in range(D)}
+
+
+def apart(T, H, D, ld_t, ld_h):
+    return len(heads_of(0, T, H, D, ld_t, ld_h)) == T * H * D and (T == 1 or ld_t >= D) and (H == 1 or ld_h >= D)
+
+
+def test_rotary_heads_that_interleave():
+    """x and y in one buffer, tokens or heads outermost, strides alike or their own, x's heads over each other too."""
+    rng = random.Random(4)
+    base, seen, alike = 1 << 33, 0, 0
+    while seen < 3000:
+        T, H, D = rng.randint(1, 4), rng.randint(1, 4), rng.randint(1, 6)
+        inner = D + rng.randint(0, 8)
+        outer = (max(T, H) - 1) * inner + D + rng.randint(0, 20)
+        ldy = (outer, inner) if rng.random() < 0.5 else (inner, outer)
+        if not apart(T, H, D, *ldy):
+            continue
+        ldx = ldy if rng.random() < 0.5 else (rng.randint(0, 30), rng.randint(0, 30))
+        at = rng.randint(0, 100) if rng.random() < 0.9 else 0
+        same = (T == 1 or ldx[0] == ldy[0]) and (H == 1 or ldx[1] == ldy[1])
+        if (at == 0 and same) or not heads_of(at, T, H, D, *ldx) & heads_of(0, T, H, D, *ldy):
+            continue
+        seen += 1
+        alike += ldx == ldy
+        assert rotary(xd=FP32, x=base + 4 * at, ld_t=ldx[0], ld_h=ldx[1], T=T, H=H, D=D, pairs=0, y=base, ldy_t=ldy[0], ldy_h=ldy[1]) == ARG, \
+            (T, H, D, ldx, ldy, at)
+    assert 500 < alike < 2500
+
+
+def test_rotary_positions_and_frequencies():
+    """4 tokens of 4 heads of 128 in bf16: 4096 bytes at A[3]; 32 of positions, 512 of frequencies."""
+    for at in (A[3] - 24, A[3], A[3] + 2048, A[3] + 4088):
+        assert rotary(pos=at) == ARG
+    for at in (A[3] - 504, A[3], A[3] + 4088):
+        assert rotary(freqs=at) == ARG
+    assert rotary(x=A[3] + 2) == ARG and rotary(x=A[3] + 4094) == ARG and rotary(x=A[3] - 4094) == ARG
+    # between y's heads there is room for a head, not for one and a value
+    assert rotary(x=A[3] + 2 * 126, ld_t=1024, ld_h=256, ldy_t=1024, ldy_h=256) == ARG
+    assert rotary(x=A[3] + 2 * 130, ld_t=1024, ld_h=256, ldy_t=1024, ldy_h=256) == ARG
