@@ -164,6 +164,6 @@ def test_heads_that_interleave(P):
             assert t.equal(buffer, before)
         else:
             clear += 1
-            want = P.puro_rotary(x.clone(), freqs)
+            want = P.puro_rotary(x.clone(memory_format=t.contiguous_format), freqs)
             assert t.equal(P.puro_rotary(x, freqs, y=y), want)
     assert clear > 50 and clash > 50
