@@ -11,8 +11,9 @@
 // and a value is coded times 448 * (1 / a), products of one reciprocal each.  Rounding to the nearest code would freeze them: a
 // step moves r by a fraction (1 - b2) / 2 of itself at rest, far less than the half step of a code, 3 to 6%.  So
 // the three bits of a code's mantissa are rounded by chance: 16 random bits are added behind them, and the sum is cut.
-// The expected value is the value itself (to 2^-17 of a code's step); the noise that remains, a random walk held back by the
-// decay, is about sqrt(half a step) = 20% of r.  Values below the codes' normal range (2^-6 of 448 under the block's
+// Of the 20 bits that are cut the lowest four meet no random ones: the expected magnitude is the value's, less 0 to 15 2^-20 of
+// a code's step (2^-17 on average).  The noise that remains, a random walk held back by the decay, is about sqrt(half a
+// step) = 20% of r.  Values below the codes' normal range (2^-6 of 448 under the block's
 // largest) go to the nearest code.  A root that is not zero never becomes zero: m / (0 + eps) would be the step then.
 // The states' arithmetic is rounded operation by operation (no fused multiply-add), so that the codes are reproducible
 // anywhere from the formulas.

@@ -320,8 +320,8 @@ typedef struct puro_adamw_hyper {
  * eps = 0 an element whose gradients have all been zero becomes NaN (0 / 0).  A bf16 param without a master loses what
  * its rounding takes of each step.
  * The step takes m' and v' before they are rounded to 8 bits.  8-bit states are rounded by chance among the two nearest
- * three-bit mantissas, which keeps their expected value, where rounding to the nearest would freeze a state that
- * moves by less than half a code's step; the random bits depend on seed, step, the job's index in the list and the element alone.
+ * three-bit mantissas, which keeps their expected value (less than 2^-16 of a code's step below it in magnitude), where rounding
+ * to the nearest would freeze a state that moves by less than half a code's step; the random bits depend on seed, step, the job's index in the list and the element alone.
  * Values below 2^-6 of a block's codes go to the nearest code, and a root that is not zero never becomes zero.
  * A gradient that is not finite is not hidden: a NaN's element becomes NaN (its codes too), an infinity's too, and with 8-bit
  * states an infinity makes all parameters of its block NaN from the next step on.
