@@ -80,7 +80,7 @@ struct ResidualArgs {
   float scale;
   float* post_mean;        // optional
   float* post_rstd;        // optional
-  bool stream;             // filled in by the launcher: h and b are read past the caches, else (in one launch) h_out written
+  bool stream;             // filled in by the launcher: h and b are read past the caches, else (bf16, in one launch) h_out written
 };
 hipError_t launch_residual(ResidualArgs a, hipStream_t st);
 hipError_t launch_residual_quant(ResidualArgs a, hipStream_t st);
@@ -117,7 +117,7 @@ struct ResidualBwdArgs {
   float* dpost;            // with post
   int accumulate;
   float* partial;          // [blocks][2 or 3][C], the workspace
-  bool stream, past;       // filled in by the launcher: the rows are read, written past the caches
+  bool stream, past;       // filled in by the launcher: the rows are read past the caches, bf16 ones written past them
 };
 // Workgroups of the backward pass, and the fp32 vectors of C columns that each leaves in the workspace.
 int residual_bwd_blocks(int64_t T, int64_t C, bool gated);

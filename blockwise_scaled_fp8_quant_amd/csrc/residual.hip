@@ -135,7 +135,7 @@ __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void residual_kernel(Residua
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[j] = __builtin_fmaf(FULL ? f[FULL ? i : 0][j] : a.scale, v[i][j], h[j]);
       const Raw8<BF16> o = pack8<BF16>(h);
-      if (VEC && WHAT != 2 && !a.stream) {
+      if (BF16 && VEC && WHAT != 2 && !a.stream) {
         apart();
         store_raw8<BF16, VEC, VEC>(a.h_out, row * n.ldx + col[i], ok ? nv[i] : 0, o);
         apart();
@@ -202,12 +202,15 @@ hipError_t launch_fwd(const ResidualArgs& a, hipStream_t st) {
 }  // namespace
 
 // Whether a call that moves `passes` times T C elements reads past the caches and leaves them to what it writes; the
-// others write past them, which leaves what they read where it is.  The border, half the memory-side cache, is where the
-// sides meet: us, 2048 columns bf16, three sets of inputs and two of outputs in turn, without - writing past - reading past:
+// others write past them (bf16; fp32 rows are written through them at any size), which leaves what they read where it is.  The
+// border, half the memory-side cache, is where the sides meet: us, 2048 columns bf16, three sets of inputs and two of outputs in turn, without - writing past - reading past:
 //   forward (4 passes)       4096 rows 12.6 - 12.5 - 15.5, 8192 26.1 - 22.1 - 24.2, 12288 38.2 - 39.6 - 36.4, 16384 54.3 - 53.7 - 44.5
 //   backward (4)             4096 rows 16.4 - 16.0 - 19.2, 8192 28.3 - 28.4 - 29.9, 12288 41.8 - 40.8 - 40.2, 16384 52.6 - 51.5 - 50.5
 //   with gate and norm (6)   4096 rows 27.1 - 25.7 - 29.5, 8192 47.4 - 45.9 - 44.5, 12288 65.3 - 63.6 - 59.1, 16384 84.6 - 81.1 - 74.5
-// Outputs that alone fill the cache go past it too: 32768 rows with gate and norm 157 - 153 - 151, both 145.
+// fp32, which only reads past them, without - reading past: forward 4096 rows 26.0 - 28.1, 6144 41.7 - 38.5, 8192 53.8 - 49.7, 16384
+// 100.9 - 105.8; backward 29.1 - 31.6, 42.9 - 43.1, 54.2 - 54.6, 103.9 - 99.6; with gate and norm 44.3 - 48.7, 62.2 - 67.3, 85.0 - 85.5,
+// 158.0 - 155.4: there the sides meet at twice the border.
+// Outputs that alone fill the cache go past it too (bf16): 32768 rows with gate and norm 157 - 153 - 151, both 145.
 bool beyond_cache(int64_t T, int64_t C, int64_t es, int passes) {
   return T > kMemorySideCache / 2 / (C * es * passes);
 }

@@ -191,7 +191,7 @@ __global__ __launch_bounds__(kBwdThreads) void residual_bwd_kernel(ResidualBwdAr
     p[1] = add ? p[1] + hi : hi;
   };
   auto store = [&](void* base, int64_t at, int n, const float (&v)[8]) {
-    if (VEC && a.past) {
+    if (BF16 && VEC && a.past) {
       apart();
       store8<BF16, VEC, VEC>(base, at, n, v);
       apart();
