@@ -103,26 +103,33 @@ inline bool share_memory(Rows a, const Rows& b) {
 class Tensors {
  public:
   void reads(const void* p, const Rows& r) {
-    if (p && r.width > 0) in_[n_in_++] = r;
+    if (p && r.width > 0) in_[n_in_++] = Spanned{r, r.hi()};
   }
   void writes(const void* p, const Rows& r) {
-    if (p && r.width > 0) out_[n_out_++] = r;
+    if (p && r.width > 0) out_[n_out_++] = Spanned{r, r.hi()};
   }
   // Whether one that is written shares memory with another that it does not replace.
   bool clash() const {
     for (int i = 0; i < n_out_; ++i) {
-      for (int k = 0; k < n_in_; ++k) {
-        const bool replaced = out_[i].replaces && in_[k].replaces && out_[i].lo == in_[k].lo && same_strides(out_[i], in_[k]);
-        if (!replaced && share_memory(in_[k], out_[i])) return true;
-      }
+      for (int k = 0; k < n_in_; ++k)
+        if (meet(in_[k], out_[i]) && !replaced(in_[k].rows, out_[i].rows) && share_memory(in_[k].rows, out_[i].rows)) return true;
       for (int k = 0; k < i; ++k)
-        if (share_memory(out_[k], out_[i])) return true;
+        if (meet(out_[k], out_[i]) && share_memory(out_[k].rows, out_[i].rows)) return true;
     }
     return false;
   }
 
  private:
-  Rows in_[12], out_[12];
+  struct Spanned {
+    Rows rows;
+    Rows::wide end;
+  };
+  // (the spans of nearly all pairs are apart)
+  static bool meet(const Spanned& a, const Spanned& b) { return a.rows.lo < b.end && b.rows.lo < a.end; }
+  static bool replaced(const Rows& in, const Rows& out) {
+    return in.replaces && out.replaces && in.lo == out.lo && same_strides(in, out);
+  }
+  Spanned in_[12], out_[12];
   int n_in_ = 0, n_out_ = 0;
 };
 
