@@ -30,7 +30,9 @@ namespace {
 // FULL: with a gate or a norm of b (their product with the scale is one vector); else the scale alone.
 // Measured, bf16 RMS, us: 16384 x 2048 y 44.5 (6.0 TB/s; three sets of inputs and two of outputs in turn), h' and statistics
 // 33 and the codes of both orientations 23 more; one row 4 in a graph: two sums' chains and one trip to memory; 4000 x 8192
-// 59, 2000 x 16384 66 with gate and norm.  1027 x 1000 fp32 with both norms, layer, 7.5: four sums' chains.
+// 59, 2000 x 16384 66 with gate and norm.  1027 x 1000 fp32 with gate and both norms, layer, 7.7: load_vec8 chooses type,
+// alignment and end at run time, and each of its branches waits for what was loaded before, so that four vectors of two chunks
+// are eight trips to memory, one behind the other.
 // ---------------------------------------------------------------------------------------------------
 template <bool BF16, bool VEC, int LPR, int ITER, int WHAT, bool FULL>
 __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void residual_kernel(ResidualArgs a) {

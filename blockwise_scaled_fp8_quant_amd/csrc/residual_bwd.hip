@@ -23,7 +23,7 @@ namespace {
 // register's reload waits for the row that is loaded ahead.  4000 x 8192: 85 us.
 // Beyond 8192 columns the first and the last column sum stay in LDS and take a row at a time (128 KB at 16384 columns; up to
 // 12288 the weight too), and no row is loaded ahead (loading ahead: 2667 x 12288 bf16 70.5 us, FULL 111.6).  With every sum in
-// registers, which spilled, and without in turn: 2667 x 12288 bf16 91.0 and 70.4 us, FULL 199.2 and 101.5; 2000 x 16384 92.5
+// registers, which spilled, and without in turn, with a scale (dx is one output more): 2667 x 12288 bf16 91.0 and 70.4 us, FULL 199.2 and 101.5; 2000 x 16384 92.5
 // and 73.2, FULL 186.5 and 154.2 (fp32 294 and 291: FULL at that width still spills 60 to 280 bytes a lane).
 // Both have no room for runs: their launches have a workgroup for every 64 rows.
 // ---------------------------------------------------------------------------------------------------

@@ -317,7 +317,7 @@ typedef struct puro_adamw_hyper {
  *   m' = beta1 m + (1 - beta1) g,   v' = beta2 v + (1 - beta2) g g
  *   param' = param (1 - lr weight_decay) - lr / (1 - beta1^step) * m' / (sqrt(v' / (1 - beta2^step)) + eps)
  * in fp32, the hyperparameters' factors rounded once from 64 bits; squares are fp32 (gradients beyond 1.8e19 overflow).  With
- * eps = 0 an element whose gradients have all been zero becomes NaN (0 / 0).  A bf16 param without a master loses what
+ * eps = 0 an element whose gradients have all been zero becomes NaN (0 / 0); an eps below 2^-126 counts as 0.  A bf16 param without a master loses what
  * its rounding takes of each step.
  * The step takes m' and v' before they are rounded to 8 bits.  8-bit states are rounded by chance among the two nearest
  * three-bit mantissas, which keeps their expected value (less than 2^-16 of a code's step below it in magnitude), where rounding
