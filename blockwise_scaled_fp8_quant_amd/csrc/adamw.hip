@@ -39,7 +39,7 @@ constexpr int kMaxJobs = 48;
 constexpr int kThreads32 = 128, kThreads8 = 256;
 // Elements a thread takes: one round of 16 bytes of fp32, or of 8 codes, so that workgroups come and go in the order of the
 // addresses.  A launch has one for every chunk, up to its 2^32 threads.  403 M elements, us, fp32 and 8-bit states, in turn on
-// one card (others: 1836 to 1899 and 1164 to 1173): 1894 (5.96 TB/s) and 1159 (5.61); two rounds a thread 2013 and 1223; 2048 workgroups that stay 2120 and 1326; workgroups of
+// one card (others: 1836 to 1901 and 1164 to 1179): 1894 (5.96 TB/s) and 1159 (5.61); two rounds a thread 2013 and 1223; 2048 workgroups that stay 2120 and 1326; workgroups of
 // 256 and 512 threads 1920 and 1970, of 128 and 512 1183 and 1182.
 constexpr int kPer32 = 4, kPer8 = 8;
 constexpr uint32_t kMaxBlocks = 1u << 23;
